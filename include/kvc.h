@@ -47,7 +47,14 @@ extern "C" {
 
 /* Element type of query, new_key, new_value, both caches and both outputs
  * ("finite floating with matching dtype", Required behavior, bullet 1). */
-typedef enum { KVC_F32 = 0, KVC_BF16 = 1, KVC_F16 = 2 } kvc_dtype;
+typedef enum {
+    KVC_F32 = 0,
+    KVC_BF16 = 1,
+    KVC_F16 = 2,
+    /* 8-bit pool formats of kvc_append_rotary_paged and kvc_attend_paged only */
+    KVC_E4M3 = 3,
+    KVC_E5M2 = 4
+} kvc_dtype;
 
 /* Problem sizes (Required behavior, bullet 1). dtype is a kvc_dtype. */
 typedef struct {
@@ -297,6 +304,124 @@ KVC_API int kvc_attend_cache_timed(const kvc_dims *dims, int64_t num_slots, int6
                            int k_cumulative, const int32_t *slot_ids, double scale, void *out,
                            void *workspace, size_t workspace_bytes, int32_t *dev_status,
                            void *stream, void *const *events, int n_events);
+
+/*
+ * The packed, paged operators: a serving stack's append and attention on one
+ * block pool, for T = total_q packed tokens of B sequences ("ClikaRT::ops::
+ * attention_over_cache": paged block pool, packed variable-length queries,
+ * cu_seqlens, and the RoPE, softcap, sliding-window and quantised-scale options
+ * that kvc_attend_cache leaves out).
+ *
+ *   block_table   [B, max_blocks] device int32. Slot j of sequence b is row
+ *                 j % block_size of block block_table[b, j / block_size];
+ *                 the capacity is M = max_blocks * block_size.
+ *   cu_seqlens_q  [B + 1] device int32: sequence b owns rows cu[b] ..
+ *                 cu[b+1]-1 of the packed tensors, S_b of them (S_b <= max_q).
+ *                 cu[B] <= total_q; rows from cu[B] on belong to no sequence: they
+ *                 are not read, and an output's are left as they were.
+ *   seqlens_k     [B] device int32: K_b cached positions, the S_b new ones
+ *                 included: row t of sequence b is position K_b - S_b + t.
+ *   pools         [num_blocks, Hk, block_size, D] and [..., Dv], of pool_dtype:
+ *                 the dtype itself, or KVC_E4M3 / KVC_E5M2 with fp32 scales
+ *                 key_scale / value_scale [num_blocks, Hk] (a stored code c
+ *                 stands for c * scale).
+ * A sequence outside this contract (cu decreasing or past total_q, S_b > max_q,
+ * S_b > K_b, K_b > M) appends nothing, gets zero output rows where its rows lie
+ * inside the packed tensor, and sets KVC_DEV_OVERFLOW.
+ */
+typedef struct {
+    int64_t B, total_q, max_q; /* sequences; packed rows; the largest S_b */
+    int64_t Hq, Hk, D, Dv;     /* D, Dv <= 256 */
+    int64_t num_blocks, block_size, max_blocks;
+    int32_t dtype;      /* of the packed tensors and the output: a kvc_dtype up to KVC_F16 */
+    int32_t pool_dtype; /* == dtype, KVC_E4M3 or KVC_E5M2 */
+} kvc_paged_dims;
+
+/*
+ * kvc_append_rotary_paged -- writes the new tokens' keys and values into the
+ * pool, the keys turned to their positions by the rotary embedding, and
+ * returns the queries turned likewise.
+ *
+ *   rotary_dim     R, even, 0 <= R <= D: the first R elements of a query or key
+ *                  row are turned, the rest copied. Pairs (x, y) are elements
+ *                  (d, d + R/2), or (2d, 2d + 1) with interleaved = 1; a pair at
+ *                  position j becomes (x cos - y sin, y cos + x sin).
+ *   num_positions  rows of cos / sin; K_b > num_positions is outside the contract.
+ *   strides        host, 6 element strides: token and head of query, new_key and
+ *                  new_value (>= 0; the last axis is contiguous).
+ *   query, new_key, new_value   [T, Hq, D], [T, Hk, D], [T, Hk, Dv] device, dtype.
+ *   cos, sin       [num_positions, R/2] device fp32.
+ *   key_pool, value_pool, key_scale, value_scale   in place; the scales NULL
+ *                  unless the pool is in 8 bits.
+ *   out_query      [T, Hq, D] device, dtype, contiguous.
+ *
+ * Pools of the inputs' type: sums in fp32, rounded once. 8-bit pools: a touched
+ * block's scale becomes 2^e, e the least in [-100, 100] with max |x| <= 1.75 *
+ * 2^top * 2^e over its new rows (top 8 for e4m3, 15 for e5m2), but no less than the
+ * scale of the rows it already holds (none when the first new row is the
+ * block's row 0: its scale and rows on entry are then not read). Rows already held
+ * are rounded again when the scale grows. Every value stored is the exact
+ * value's, divided by the scale and rounded once, ties to even, ending at the
+ * format's largest; non-finite inputs take no part in the scale (infinities are
+ * stored as the largest, NaN as NaN). A held scale that is no power of two is
+ * kept while it suffices; values are then divided in fp32 first.
+ *
+ * A sequence whose table has an id outside [0, num_blocks) among its new
+ * slots' blocks is outside the contract too. The blocks that sequences write
+ * must be distinct, and no other call may use them at the same time. No workspace;
+ * the outputs and pools may not overlap any other argument (KVC_E_ALIAS).
+ */
+KVC_API int kvc_append_rotary_paged(const kvc_paged_dims *dims, int64_t rotary_dim,
+                                    int64_t num_positions, int32_t interleaved,
+                                    const int64_t *strides, const void *query,
+                                    const void *new_key, const void *new_value,
+                                    const int32_t *block_table, const int32_t *cu_seqlens_q,
+                                    const int32_t *seqlens_k, const float *cos, const float *sin,
+                                    void *key_pool, void *value_pool, float *key_scale,
+                                    float *value_scale, void *out_query, int32_t *dev_status,
+                                    void *stream);
+
+/*
+ * kvc_attend_paged -- read-only attention of packed queries over the pool.
+ *
+ * Query row (t, h) of sequence b, at position p = K_b - S_b + t, sees the slots
+ * j <= p with j > p - window (window 0: no such limit). Its scores are
+ * s = scale * q.k_j; with softcap > 0, softcap * tanh(s / softcap); with
+ * alibi_slopes, less alibi_slopes[h] * (p - j). out = softmax(s) . v.
+ *
+ *   q_strides     host, 2 element strides: token and head (the last axis contiguous).
+ *   q             [T, Hq, D] device, dtype.
+ *   softcap       >= 0, finite; 0: no cap.
+ *   alibi_slopes  [Hq] device fp32, nullable.
+ *   window        >= 0; 0: none. Blocks wholly before a window are not read.
+ *   key_scale, value_scale   NULL unless the pool is in 8 bits; then positive,
+ *                 within 2^-100 .. 2^100.
+ *   out           [T, Hq, Dv] device, dtype, contiguous.
+ *   workspace     >= kvc_attend_paged_workspace_bytes(dims), 16-byte aligned;
+ *                 contents on entry do not matter. One call at a time uses it.
+ *
+ * A masked slot's key and value never enter, whatever they hold. A query row
+ * that would read a block id outside [0, num_blocks) gets a zero row and
+ * KVC_DEV_OVERFLOW is set; other rows of that sequence are right or zero.
+ * The softmax sums are fp32. kvc_attend_paged_path names the kernel that the
+ * sizes take and its roundings; the others round the result alone.
+ */
+KVC_API size_t kvc_attend_paged_workspace_bytes(const kvc_paged_dims *dims);
+
+KVC_API int kvc_attend_paged(const kvc_paged_dims *dims, const int64_t *q_strides, const void *q,
+                             const void *key_pool, const void *value_pool, const float *key_scale,
+                             const float *value_scale, const int32_t *block_table,
+                             const int32_t *cu_seqlens_q, const int32_t *seqlens_k, double scale,
+                             double softcap, const float *alibi_slopes, int64_t window, void *out,
+                             void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                             void *stream);
+
+/*
+ * The kernel kvc_attend_paged takes for these sizes with 16-byte aligned pools
+ * and queries: "cores" (CUDA cores: any size). Static text, or NULL for invalid
+ * dims.
+ */
+KVC_API const char *kvc_attend_paged_path(const kvc_paged_dims *dims);
 
 /*
  * kvc_step_static -- kvc_step for callers that cannot allocate device memory.

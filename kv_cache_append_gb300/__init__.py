@@ -14,8 +14,11 @@ from .kvc import (DEV_MASK, DEV_OVERFLOW, DEV_TIMEOUT, DTYPES, Dims, KvcError,  
                   step_paged_into,
                   make_dims, plan_info, plan_info_inplace, selftest_wait_timeout, status_string,
                   step_inplace_into, step_into, workspace_bytes)
+from .paged import (EIGHT_BIT, PagedDims, append_rotary_paged,  # noqa: F401
+                    attend_paged_path, attend_paged_workspace_bytes, attention_over_paged_cache,
+                    make_paged_dims)
 
 __all__ = ["kv_cache_attention_step", "kv_cache_attention_step_inplace",
            "kv_cache_attention_step_paged", "kv_cache_attention_step_backward",
-           "attention_over_cache", "KvcError",
+           "attention_over_cache", "append_rotary_paged", "attention_over_paged_cache", "KvcError",
            "workspace_bytes", "step_into", "step_inplace_into", "library"]

@@ -151,4 +151,65 @@ cudaError_t launch_attend_unpack(const AttendParams& a, cudaStream_t stream);
 cudaError_t launch_generic_copy(const StepParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_generic_attend(const StepParams& p, int dtype, cudaStream_t stream);
 
+// ------------------------------------------------ packed, paged operators
+// Rotary append into a paged pool (kvc_rotary_append.cu).
+constexpr int kMaxTokensPerBlock = 16;
+struct AppendParams {
+    int64_t B, total_q, max_q, M, max_blocks;
+    int num_blocks, Hq, Hk, D, Dv, bs;
+    int half;         // rotated pairs of a row
+    int num_pos;      // rows of the angle tables
+    int interleaved;
+    int64_t st[6];    // element strides of a token and a head: query, new_key, new_value
+    const void* query;
+    const void* new_key;
+    const void* new_value;
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* kl;
+    const float* cos;
+    const float* sin;
+    void* key_pool;
+    void* value_pool;
+    float* key_scale;
+    float* value_scale;
+    void* out_query;
+    int32_t* status;
+    int tpb;              // tokens per block of the first tok_blocks blocks
+    unsigned tok_blocks;
+    int64_t seq_blocks;   // 8-bit pools: pool blocks a sequence can touch
+    int64_t units8;       // 8-bit pools: B * seq_blocks * Hk * 2, else 0
+};
+// kind 0: pools of the inputs' type, 1: e4m3, 2: e5m2. ve: elements per access.
+cudaError_t launch_append_rotary(const AppendParams& p, int dtype, int kind, int ve,
+                                 cudaStream_t stream);
+
+// Read-only attention of packed queries over a paged pool.
+struct PagedAttendParams {
+    int64_t B, total_q, max_q, M, max_blocks;
+    int num_blocks, Hq, Hk, G, D, Dv, bs;
+    int64_t q_tok, q_head;  // element strides of a query token and head
+    const void* q;
+    const void* kp;
+    const void* vp;
+    const float* ks;      // scale per (block, head); NULL: pools of the queries' type
+    const float* vs;
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* kl;
+    const float* slopes;  // per query head; NULL: no bias
+    float scale, softcap; // softcap 0: none
+    int window;           // 0: none
+    void* out;
+    int32_t* status;
+    int e5m2;
+    // CUDA-core kernel: KV splits and their length
+    int nsplit, split_len;
+    float* part_ml;       // CUDA cores: [nsplit][total_q][Hq][2]
+    float* part_acc;      // [nsplit][total_q][Hq][Dv]
+};
+// CUDA cores, any type and size up to 256 (kvc_paged_attend.cu).
+cudaError_t launch_paged_attend(const PagedAttendParams& p, int dtype, int pool_dtype,
+                                cudaStream_t stream);
+
 }  // namespace kvc

@@ -1,0 +1,247 @@
+// kvc_paged_api.cu -- C entry points of the packed, paged operators
+// (include/kvc.h): argument checks and launch plans. Nothing here allocates or
+// synchronises.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "kvc_launch.h"
+
+namespace kvc {
+namespace {
+
+// Splits and grids are planned for this many SMs, so that the workspace size
+// does not depend on the device.
+constexpr int64_t kPlanSms = 152;
+constexpr int64_t kMaxInt = int64_t(1) << 30;
+
+struct Range {
+    uintptr_t lo, hi;
+};
+Range range_of(const void* p, int64_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return Range{a, a + static_cast<uintptr_t>(bytes > 0 && p ? bytes : 0)};
+}
+bool overlaps(Range a, Range b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+bool aligned(const void* p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int elem(int32_t dtype) {
+    return dtype == KVC_F32 ? 4 : (dtype == KVC_E4M3 || dtype == KVC_E5M2) ? 1 : 2;
+}
+bool eight(const kvc_paged_dims& d) { return d.pool_dtype != d.dtype; }
+
+int check_paged(const kvc_paged_dims* dims) {
+    if (!dims) return KVC_E_NULL;
+    const kvc_paged_dims& d = *dims;
+    if (d.dtype < KVC_F32 || d.dtype > KVC_F16 ||
+        (d.pool_dtype != d.dtype && d.pool_dtype != KVC_E4M3 && d.pool_dtype != KVC_E5M2))
+        return KVC_E_DTYPE;
+    if (d.B < 1 || d.total_q < 0 || d.max_q < 0 || d.Hq < 1 || d.Hk < 1 || d.Hq % d.Hk != 0 ||
+        d.D < 1 || d.Dv < 1 || d.D > 256 || d.Dv > 256 || d.num_blocks < 1 || d.block_size < 1 ||
+        d.max_blocks < 1 || (d.total_q > 0 && d.max_q < 1))
+        return KVC_E_SHAPE;
+    // device code counts rows, slots and blocks in 31 bits, bytes in 64
+    if (d.B > kMaxInt || d.Hq > 65535 || d.num_blocks > kMaxInt / d.Hk ||
+        d.block_size > kMaxInt || d.max_blocks > kMaxInt / d.block_size ||
+        d.total_q > kMaxInt / d.Hq || d.max_q > kMaxInt / d.Hq || d.B > kMaxInt / d.Hq)
+        return KVC_E_SHAPE;
+    return KVC_OK;
+}
+
+int64_t span(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t w, int64_t es) {
+    return n0 < 1 ? 0 : ((n0 - 1) * s0 + (n1 - 1) * s1 + w) * es;
+}
+
+bool current_is_gb300() {
+    int dev = 0, major = 0, minor = 0;
+    return cudaGetDevice(&dev) == cudaSuccess &&
+           cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
+           cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
+           major == 10 && minor == 3;
+}
+
+// The CUDA-core kernel's splits of the slots: enough blocks for every SM to
+// hold a few, each with 256 slots or more of the capacity.
+struct CorePlan {
+    int64_t nsplit, split_len, bytes;
+};
+CorePlan core_plan(const kvc_paged_dims& d) {
+    const int64_t G = d.Hq / d.Hk, M = d.max_blocks * d.block_size;
+    const int64_t blocks = std::max<int64_t>(1, d.B * ((d.max_q * G + 7) / 8) * d.Hk);
+    CorePlan c;
+    c.nsplit = std::max<int64_t>(1, std::min({(4 * kPlanSms + blocks - 1) / blocks, M / 256,
+                                              int64_t(64), 65535 / d.Hk}));
+    c.split_len = (M + c.nsplit - 1) / c.nsplit;
+    c.bytes = c.nsplit > 1 ? c.nsplit * d.total_q * d.Hq * (d.Dv + 2) * 4 : 0;
+    return c;
+}
+
+}  // namespace
+}  // namespace kvc
+
+extern "C" {
+
+int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int64_t num_positions,
+                            int32_t interleaved, const int64_t* strides, const void* query,
+                            const void* new_key, const void* new_value, const int32_t* block_table,
+                            const int32_t* cu_seqlens_q, const int32_t* seqlens_k, const float* cos,
+                            const float* sin, void* key_pool, void* value_pool, float* key_scale,
+                            float* value_scale, void* out_query, int32_t* dev_status,
+                            void* stream_ptr) {
+    using namespace kvc;
+    const int rc = check_paged(dims);
+    if (rc != KVC_OK) return rc;
+    const kvc_paged_dims d = *dims;
+    const int64_t T = d.total_q, es = elem(d.dtype), ps = elem(d.pool_dtype);
+    if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > d.D || num_positions < 0 ||
+        num_positions > kMaxInt || (interleaved != 0 && interleaved != 1))
+        return KVC_E_SHAPE;
+    const int64_t half = rotary_dim / 2;
+    if (!strides || !block_table || !cu_seqlens_q || !seqlens_k || !key_pool || !value_pool ||
+        (T > 0 && (!query || !new_key || !new_value || !out_query)) ||
+        (half > 0 && num_positions > 0 && (!cos || !sin)) ||
+        (eight(d) ? (!key_scale || !value_scale) : (key_scale || value_scale)))
+        return KVC_E_NULL;
+    for (int i = 0; i < 6; ++i)
+        if (strides[i] < 0 || strides[i] > (int64_t(1) << 40)) return KVC_E_SHAPE;
+    const int64_t rows = d.num_blocks * d.Hk * d.block_size;
+    const Range ins[] = {
+        range_of(query, span(T, strides[0], d.Hq, strides[1], d.D, es)),
+        range_of(new_key, span(T, strides[2], d.Hk, strides[3], d.D, es)),
+        range_of(new_value, span(T, strides[4], d.Hk, strides[5], d.Dv, es)),
+        range_of(block_table, d.B * d.max_blocks * 4),
+        range_of(cu_seqlens_q, (d.B + 1) * 4),
+        range_of(seqlens_k, d.B * 4),
+        range_of(cos, num_positions * half * 4),
+        range_of(sin, num_positions * half * 4),
+    };
+    const Range outs[] = {
+        range_of(key_pool, rows * d.D * ps),
+        range_of(value_pool, rows * d.Dv * ps),
+        range_of(out_query, T * d.Hq * d.D * es),
+        range_of(key_scale, d.num_blocks * d.Hk * 4),
+        range_of(value_scale, d.num_blocks * d.Hk * 4),
+    };
+    for (int i = 0; i < 5; ++i) {
+        for (const Range& r : ins)
+            if (overlaps(outs[i], r)) return KVC_E_ALIAS;
+        for (int k = 0; k < i; ++k)
+            if (overlaps(outs[i], outs[k])) return KVC_E_ALIAS;
+    }
+    if (!current_is_gb300()) return KVC_E_DEVICE;
+    if (T == 0) return KVC_OK;
+
+    AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.B = d.B; p.total_q = T; p.max_q = d.max_q; p.M = d.max_blocks * d.block_size;
+    p.max_blocks = d.max_blocks; p.num_blocks = static_cast<int>(d.num_blocks);
+    p.Hq = static_cast<int>(d.Hq); p.Hk = static_cast<int>(d.Hk);
+    p.D = static_cast<int>(d.D); p.Dv = static_cast<int>(d.Dv); p.bs = static_cast<int>(d.block_size);
+    p.half = static_cast<int>(half); p.num_pos = half ? static_cast<int>(num_positions) : 0x7fffffff;
+    p.interleaved = interleaved;
+    std::copy(strides, strides + 6, p.st);
+    p.query = query; p.new_key = new_key; p.new_value = new_value;
+    p.table = block_table; p.cu = cu_seqlens_q; p.kl = seqlens_k; p.cos = cos; p.sin = sin;
+    p.key_pool = key_pool; p.value_pool = value_pool;
+    p.key_scale = key_scale; p.value_scale = value_scale;
+    p.out_query = out_query; p.status = dev_status;
+    // the widest access (16 bytes of a 16-bit type, or 8, or one element) that
+    // every row, stride and pointer allows
+    int ve = es == 2 ? 8 : 4;
+    auto fits = [&](int64_t v) {
+        bool ok = half % v == 0 && (d.D - rotary_dim) % v == 0 && d.Dv % v == 0 && d.D % v == 0 &&
+                  aligned(cos, 16) && aligned(sin, 16) && aligned(key_pool, v * ps) &&
+                  aligned(value_pool, v * ps) && aligned(out_query, v * es) &&
+                  aligned(query, v * es) && aligned(new_key, v * es) && aligned(new_value, v * es);
+        for (int i = 0; i < 6; ++i) ok = ok && strides[i] % v == 0;
+        return ok;
+    };
+    while (ve > 1 && !fits(ve)) ve = ve == 8 ? 4 : 1;
+    // a block per token while blocks are few; then several, so that the look-up of
+    // a token's sequence and slot is paid for once per block's worth of loads
+    p.tpb = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxTokensPerBlock,
+                                                                    T / (8 * kPlanSms))));
+    p.tok_blocks = static_cast<unsigned>((T + p.tpb - 1) / p.tpb);
+    if (eight(d)) {
+        p.seq_blocks = std::min<int64_t>((d.max_q + d.block_size - 2) / d.block_size + 1, d.max_blocks);
+        p.units8 = d.B * p.seq_blocks * d.Hk * 2;
+    }
+    return launch_append_rotary(p, d.dtype, d.pool_dtype == KVC_E4M3 ? 1 : d.pool_dtype == KVC_E5M2 ? 2 : 0,
+                                ve, static_cast<cudaStream_t>(stream_ptr)) == cudaSuccess
+               ? KVC_OK : KVC_E_CUDA;
+}
+
+const char* kvc_attend_paged_path(const kvc_paged_dims* dims) {
+    return kvc::check_paged(dims) == KVC_OK ? "cores" : nullptr;
+}
+
+size_t kvc_attend_paged_workspace_bytes(const kvc_paged_dims* dims) {
+    if (kvc::check_paged(dims) != KVC_OK) return 0;
+    return static_cast<size_t>((kvc::core_plan(*dims).bytes + 255) / 256 * 256 + 256);
+}
+
+int kvc_attend_paged(const kvc_paged_dims* dims, const int64_t* q_strides, const void* q,
+                     const void* key_pool, const void* value_pool, const float* key_scale,
+                     const float* value_scale, const int32_t* block_table,
+                     const int32_t* cu_seqlens_q, const int32_t* seqlens_k, double scale,
+                     double softcap, const float* alibi_slopes, int64_t window, void* out,
+                     void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                     void* stream_ptr) {
+    using namespace kvc;
+    const int rc = check_paged(dims);
+    if (rc != KVC_OK) return rc;
+    const kvc_paged_dims d = *dims;
+    const int64_t T = d.total_q, es = elem(d.dtype), ps = elem(d.pool_dtype);
+    if (window < 0) return KVC_E_SHAPE;
+    if (!q_strides || !key_pool || !value_pool || !block_table || !cu_seqlens_q || !seqlens_k ||
+        (T > 0 && (!q || !out)) ||
+        (eight(d) ? (!key_scale || !value_scale) : (key_scale || value_scale)))
+        return KVC_E_NULL;
+    if (!(scale > 0.0) || !std::isfinite(scale) || !(softcap >= 0.0) || !std::isfinite(softcap) ||
+        !std::isfinite(static_cast<float>(scale)) || !std::isfinite(static_cast<float>(softcap)))
+        return KVC_E_SCALE;
+    for (int i = 0; i < 2; ++i)
+        if (q_strides[i] < 0 || q_strides[i] > (int64_t(1) << 40)) return KVC_E_SHAPE;
+    const size_t need = kvc_attend_paged_workspace_bytes(dims);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return KVC_E_WORKSPACE;
+    const int64_t rows = d.num_blocks * d.Hk * d.block_size;
+    const Range ins[] = {
+        range_of(q, span(T, q_strides[0], d.Hq, q_strides[1], d.D, es)),
+        range_of(key_pool, rows * d.D * ps),
+        range_of(value_pool, rows * d.Dv * ps),
+        range_of(key_scale, d.num_blocks * d.Hk * 4),
+        range_of(value_scale, d.num_blocks * d.Hk * 4),
+        range_of(block_table, d.B * d.max_blocks * 4),
+        range_of(cu_seqlens_q, (d.B + 1) * 4),
+        range_of(seqlens_k, d.B * 4),
+        range_of(alibi_slopes, d.Hq * 4),
+    };
+    const Range o = range_of(out, T * d.Hq * d.Dv * es);
+    const Range w = range_of(workspace, static_cast<int64_t>(need));
+    if (overlaps(o, w)) return KVC_E_ALIAS;
+    for (const Range& r : ins)
+        if (overlaps(o, r) || overlaps(w, r)) return KVC_E_ALIAS;
+    if (!current_is_gb300()) return KVC_E_DEVICE;
+    if (T == 0) return KVC_OK;
+
+    const CorePlan c = core_plan(d);
+    PagedAttendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.B = d.B; p.total_q = T; p.max_q = d.max_q; p.M = d.max_blocks * d.block_size;
+    p.max_blocks = d.max_blocks; p.num_blocks = static_cast<int>(d.num_blocks);
+    p.Hq = static_cast<int>(d.Hq); p.Hk = static_cast<int>(d.Hk); p.G = static_cast<int>(d.Hq / d.Hk);
+    p.D = static_cast<int>(d.D); p.Dv = static_cast<int>(d.Dv); p.bs = static_cast<int>(d.block_size);
+    p.q_tok = q_strides[0]; p.q_head = q_strides[1];
+    p.q = q; p.kp = key_pool; p.vp = value_pool; p.ks = key_scale; p.vs = value_scale;
+    p.table = block_table; p.cu = cu_seqlens_q; p.kl = seqlens_k; p.slopes = alibi_slopes;
+    p.scale = static_cast<float>(scale); p.softcap = static_cast<float>(softcap);
+    p.window = window >= p.M ? 0 : static_cast<int>(window);
+    p.out = out; p.status = dev_status; p.e5m2 = d.pool_dtype == KVC_E5M2;
+    p.nsplit = static_cast<int>(c.nsplit); p.split_len = static_cast<int>(c.split_len);
+    p.part_ml = static_cast<float*>(workspace);
+    p.part_acc = p.part_ml + 2 * c.nsplit * T * d.Hq;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    return launch_paged_attend(p, d.dtype, d.pool_dtype, stream) == cudaSuccess ? KVC_OK : KVC_E_CUDA;
+}
+
+}  // extern "C"
