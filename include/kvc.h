@@ -403,8 +403,8 @@ KVC_API int kvc_append_rotary_paged(const kvc_paged_dims *dims, int64_t rotary_d
  * A masked slot's key and value never enter, whatever they hold. A query row
  * that would read a block id outside [0, num_blocks) gets a zero row and
  * KVC_DEV_OVERFLOW is set; other rows of that sequence are right or zero.
- * The softmax sums are fp32. kvc_attend_paged_path names the kernel that the
- * sizes take and its roundings; the others round the result alone.
+ * The softmax sums are fp32; what is rounded besides the result: see
+ * kvc_attend_paged_path.
  */
 KVC_API size_t kvc_attend_paged_workspace_bytes(const kvc_paged_dims *dims);
 
@@ -418,8 +418,13 @@ KVC_API int kvc_attend_paged(const kvc_paged_dims *dims, const int64_t *q_stride
 
 /*
  * The kernel kvc_attend_paged takes for these sizes with 16-byte aligned pools
- * and queries: "cores" (CUDA cores: any size). Static text, or NULL for invalid
- * dims.
+ * and queries: "decode" (tensor cores: at most 32 query rows max_q * Hq / Hk of a
+ * KV head; 16-bit queries, rows of whole 16-byte words, D <= 256, Dv <= 128,
+ * block_size a multiple of 8) or "cores" (CUDA cores: any size). Static text, or
+ * NULL for invalid dims. With an 8-bit pool the tensor-core kernels take a query
+ * element as the sum of two e4m3 values (off by at most 2^-8 of it, or 2^-18 of
+ * the row's largest) and a softmax weight as e4m3 + e5m2 (2^-7); with 16-bit
+ * pools a weight is rounded to the dtype.
  */
 KVC_API const char *kvc_attend_paged_path(const kvc_paged_dims *dims);
 

@@ -212,4 +212,29 @@ struct PagedAttendParams {
 cudaError_t launch_paged_attend(const PagedAttendParams& p, int dtype, int pool_dtype,
                                 cudaStream_t stream);
 
+// Tensor-core kernels of the paged attention (kvc_paged_tc.cuh): the pools as
+// [num_blocks * Hk][block_size][width] tensor maps (boxes of 128 bytes x hh
+// slots, 128-byte swizzle), the layout of shared memory and the workspace.
+struct PagedRec {
+    int valid, q0, r0, hk, rows, c0, c1, pad;
+};
+struct PagedTcParams {
+    CUtensorMap tk, tv;
+    PagedAttendParams a;
+    int RG;            // query rows of a unit
+    int ctas;          // blocks of the grid
+    int hh;            // slots of a box: the largest power of two up to 128 dividing block_size
+    int ns, ni;        // stages, item (and query) buffers
+    int off_item, off_q, off_x, off_p, off_stage;  // shared memory
+    int q_bytes, stage_bytes;
+    float* part_ml;    // [2 ctas][RG][2]
+    float* part_acc;   // [2 ctas][RG][Dv]
+    PagedRec* rec;     // [ctas]
+};
+// Units of up to 32 query rows; nr: 4, 8, 16 or 32 (>= the rows of a unit).
+cudaError_t launch_paged_decode(const PagedTcParams& p, int dtype, int pool_dtype, int nr,
+                                size_t smem, cudaStream_t stream);
+// The partials of units cut between blocks.
+cudaError_t launch_paged_merge(const PagedTcParams& p, int dtype, cudaStream_t stream);
+
 }  // namespace kvc

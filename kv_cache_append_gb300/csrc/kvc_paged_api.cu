@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "kvc_launch.h"
 
@@ -74,6 +75,97 @@ CorePlan core_plan(const kvc_paged_dims& d) {
     c.split_len = (M + c.nsplit - 1) / c.nsplit;
     c.bytes = c.nsplit > 1 ? c.nsplit * d.total_q * d.Hq * (d.Dv + 2) * 4 : 0;
     return c;
+}
+
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+// The tensor-core kernels: 16-bit queries, rows of whole 16-byte words, keys up
+// to 256 and values up to 128 wide, blocks of a multiple of 8 slots (a box
+// then starts on an 8-row swizzle atom).
+struct TcPlan {
+    bool ok = false;
+    int nr = 0;  // decode kernel: rows a unit is padded to
+    size_t smem = 0;
+    int64_t bytes = 0, off_ml = 0, off_acc = 0;
+    PagedTcParams p;
+};
+constexpr int64_t kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024, kSmemReserved = 1024;
+
+TcPlan tc_plan(const kvc_paged_dims& d) {
+    TcPlan t;
+    const int64_t es = elem(d.pool_dtype), R = d.max_q * (d.Hq / d.Hk);
+    if (d.dtype == KVC_F32 || d.D * es % 16 != 0 || d.Dv * es % 16 != 0 || d.Dv > 128 ||
+        d.block_size % 8 != 0 || R > 32 || d.total_q < 1)
+        return t;
+    std::memset(&t.p, 0, sizeof(t.p));
+    PagedTcParams& p = t.p;
+    t.nr = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
+    const int64_t dn = t.nr <= 16 ? 16 : 32, parts = es == 1 ? 2 : 1;
+    const int64_t nkb = (d.D * es + 127) / 128, nvb = es == 1 ? 1 : 2, nblk = dn * 128;
+    p.RG = t.nr;
+    p.hh = 128;
+    while (d.block_size % p.hh != 0) p.hh /= 2;
+    p.stage_bytes = static_cast<int>((nkb + nvb) * 128 * 128);
+    p.q_bytes = static_cast<int>(up(parts * nkb * nblk + 32 * 12, 1024));
+    const int64_t npt = es == 2 && dn == 16 ? 2 : 1;
+    p.ni = 2;
+    p.off_item = 2048;
+    p.off_x = 2048 + 256;
+    p.off_q = static_cast<int>(up(p.off_x + 2 * t.nr * 16 + 32, 1024));
+    p.off_p = p.off_q + p.ni * p.q_bytes;
+    p.off_stage = static_cast<int>(p.off_p + npt * parts * (es == 1 ? 1 : 2) * nblk);
+    // two blocks an SM where each still has two stages or more (not for 32 rows,
+    // whose registers take a whole SM)
+    int64_t blocks = es == 1 && t.nr <= 16 ? 2 : 1;
+    int64_t room = kSmemSm / blocks - kSmemReserved - p.off_stage;
+    if (blocks == 2 && room < 2 * p.stage_bytes) blocks = 1;
+    if (blocks == 1) room = kSmemBlock - p.off_stage;
+    p.ns = static_cast<int>(std::min<int64_t>(8, room / p.stage_bytes));
+    if (p.ns < 2) return t;
+    t.smem = static_cast<size_t>(p.off_stage + int64_t(p.ns) * p.stage_bytes);
+    p.ctas = static_cast<int>(kPlanSms * blocks);
+    t.off_ml = up(p.ctas * static_cast<int64_t>(sizeof(PagedRec)), 256);
+    t.off_acc = t.off_ml + up(int64_t(2) * p.ctas * p.RG * 8, 256);
+    t.bytes = t.off_acc + int64_t(2) * p.ctas * p.RG * d.Dv * 4;
+    t.ok = true;
+    return t;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+// A pool as [num_blocks * Hk][block_size][width], boxes of 128 bytes x hh slots.
+bool pool_map(CUtensorMap* map, const void* base, const kvc_paged_dims& d, int64_t width, int hh) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const int64_t es = elem(d.pool_dtype);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(d.block_size),
+                                static_cast<cuuint64_t>(d.num_blocks * d.Hk)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width * es),
+                                   static_cast<cuuint64_t>(d.block_size * width * es)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(hh), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType type = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : d.dtype == KVC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -172,12 +264,15 @@ int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int6
 }
 
 const char* kvc_attend_paged_path(const kvc_paged_dims* dims) {
-    return kvc::check_paged(dims) == KVC_OK ? "cores" : nullptr;
+    if (kvc::check_paged(dims) != KVC_OK) return nullptr;
+    return kvc::tc_plan(*dims).ok ? "decode" : "cores";
 }
 
 size_t kvc_attend_paged_workspace_bytes(const kvc_paged_dims* dims) {
     if (kvc::check_paged(dims) != KVC_OK) return 0;
-    return static_cast<size_t>((kvc::core_plan(*dims).bytes + 255) / 256 * 256 + 256);
+    // enough for either kernel: which one runs also depends on the pointers
+    return static_cast<size_t>(
+        kvc::up(std::max(kvc::core_plan(*dims).bytes, kvc::tc_plan(*dims).bytes), 256) + 256);
 }
 
 int kvc_attend_paged(const kvc_paged_dims* dims, const int64_t* q_strides, const void* q,
@@ -237,10 +332,26 @@ int kvc_attend_paged(const kvc_paged_dims* dims, const int64_t* q_strides, const
     p.scale = static_cast<float>(scale); p.softcap = static_cast<float>(softcap);
     p.window = window >= p.M ? 0 : static_cast<int>(window);
     p.out = out; p.status = dev_status; p.e5m2 = d.pool_dtype == KVC_E5M2;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    TcPlan t = tc_plan(d);
+    // the tensor-core kernels read query rows in words of 8 bytes (split into
+    // 8-bit parts) or 16 (copied)
+    const int64_t qw = eight(d) ? 8 : 16;
+    if (t.ok && aligned(key_pool, 16) && aligned(value_pool, 16) && aligned(q, qw) &&
+        q_strides[0] * es % qw == 0 && q_strides[1] * es % qw == 0 &&
+        pool_map(&t.p.tk, key_pool, d, d.D, t.p.hh) && pool_map(&t.p.tv, value_pool, d, d.Dv, t.p.hh)) {
+        unsigned char* ws = static_cast<unsigned char*>(workspace);
+        t.p.a = p;
+        t.p.rec = reinterpret_cast<PagedRec*>(ws);
+        t.p.part_ml = reinterpret_cast<float*>(ws + t.off_ml);
+        t.p.part_acc = reinterpret_cast<float*>(ws + t.off_acc);
+        cudaError_t e = launch_paged_decode(t.p, d.dtype, d.pool_dtype, t.nr, t.smem, stream);
+        if (e == cudaSuccess) e = launch_paged_merge(t.p, d.dtype, stream);
+        return e == cudaSuccess ? KVC_OK : KVC_E_CUDA;
+    }
     p.nsplit = static_cast<int>(c.nsplit); p.split_len = static_cast<int>(c.split_len);
     p.part_ml = static_cast<float*>(workspace);
     p.part_acc = p.part_ml + 2 * c.nsplit * T * d.Hq;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     return launch_paged_attend(p, d.dtype, d.pool_dtype, stream) == cudaSuccess ? KVC_OK : KVC_E_CUDA;
 }
 

@@ -1,0 +1,852 @@
+// kvc_paged_decode.cu -- attention over a paged pool on the tensor cores, for
+// units (sequence, KV head) of at most 32 query rows: decode and short
+// speculative steps.
+//
+// A step reads each visible cache row once and does 2 R (D + Dv) operations on
+// it: memory bounds it once the arithmetic is off the CUDA cores. As in the
+// decode kernel of the step, a tile's 128 slots are the M dimension of both
+// products, the unit's rows (padded to N = 16 or 32) the N dimension:
+//
+//   S^T  = K Q^T      (A = K tile as TMA wrote it, B = query rows)
+//   O^T += V^T P^T    (A = V tile read M-major, B = P^T from shared memory)
+//
+// 8-bit pools go to the tensor cores as they lie in memory (kind::f8f6f4), with
+// no conversion: the other operand is split into two 8-bit parts, and the
+// products of both parts add up in the same accumulator.
+//   Query rows: x 2^k = hi + lo, both e4m3, k from the row's largest element
+//   (2^7..2^8 then). 4 + 4 significant bits: bf16 exactly, fp16 to 2^-8 of an element.
+//   Weights: w = hi (e4m3) + lo (e5m2). lo takes what hi leaves, down to 2^-17
+//   where e4m3 ends at 2^-10; with w up to 2^8.75 a weight is exact to 2^-7
+//   over 2^18 below the largest and not lost before 2^25 below it. (Two e4m3 parts
+//   would drop weights 2^-18 below the largest: the flat rest behind one dominant
+//   slot of a long context.)
+// The key scale of a slot's block multiplies its scores. The value scale goes into
+// the weight: w = 2^(s + log2 vs - ref), and the row sum takes w / vs, so one
+// reference per row bounds the weights whatever the blocks' scales are.
+// N is padded to 16 anyway, so the second part costs nothing that matters: the
+// tensor cores are idle most of the time.
+//
+// Warps: 4 softmax warps (a thread owns a slot), one S issuer, one P.V issuer,
+// one producer (block-table look-ups, scales, TMA boxes), one scheduler, which walks
+// the block's runs (kvc_paged_tc.cuh) and splits the next run's query rows
+// while the others work on the current one. 8-bit tiles of D = Dv = 128 are 32
+// KB, so two blocks fit an SM with three stages each and cover each
+// other's softmax latency; 16-bit tiles take one block an SM.
+//
+// A slot that no row sees has its value row set to zero in the tile. A
+// slot that some rows see and others do not (the newest tokens, a window's edge)
+// could carry an infinity or NaN into the rows that do not: its thread then
+// clears those elements in the tile and the unit's epilogue adds them, from
+// memory, to the rows that see them.
+#include <algorithm>
+#include <type_traits>
+
+#include "kvc_paged_tc.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kTS = 128;
+constexpr int kMmaWarp = 4, kPvWarp = 5, kProdWarp = 6;  // warp 7 schedules
+constexpr int kThreads = 8 * 32;
+constexpr float kOffset = 7.f;  // weights are 2^(s - ref + 7)
+
+template <int EB>
+struct Threshold {
+    // a row's reference is raised when a score exceeds it by more: 8-bit weights
+    // end at 448 = 2^8.8, 16-bit ones at 2^15 and more
+    static constexpr float v = EB == 1 ? 1.75f : 8.f;
+};
+
+struct Bars {
+    uint32_t base;
+    __device__ uint32_t full(int s) const { return base + 8u * s; }
+    __device__ uint32_t empty(int s) const { return base + 64u + 8u * s; }
+    __device__ uint32_t item_full(int k) const { return base + 128u + 8u * k; }
+    __device__ uint32_t item_empty(int k) const { return base + 160u + 8u * k; }
+    __device__ uint32_t s_ready(int b) const { return base + 192u + 8u * b; }
+    __device__ uint32_t s_free(int b) const { return base + 208u + 8u * b; }
+    __device__ uint32_t p_ready(int b) const { return base + 224u + 8u * b; }
+    __device__ uint32_t o_done(int b) const { return base + 240u + 8u * b; }
+    __device__ uint32_t meet() const { return base + 256u; }
+    __device__ uint32_t drained() const { return base + 264u; }
+};
+constexpr int kTmemSlot = 272, kAbort = 276, kBad = 280 /* [4] */, kOdd = 296 /* [2] */;
+// PagedStart at 512 (32 sums and 4 words), StageScales from 1024
+
+// What a run's query buffer holds behind the rows: per row the factor of its
+// products, its position (-1: no row) and its bias slope (times log2 e).
+struct RowData {
+    float mul[32];
+    int lim[32];
+    float slope[32];
+};
+
+template <int EB, int DN>
+struct Shape {
+    static constexpr int kParts = EB == 1 ? 2 : 1;         // of a query row, and of a weight
+    static constexpr int nblk = DN * 128;                  // a 128-byte column block of Q or P^T
+    static constexpr int pblks = EB == 1 ? 1 : 2;          // column blocks of 128 weights
+    static constexpr int pbytes = kParts * pblks * nblk;   // one P^T buffer
+    static constexpr int npt = (EB == 2 && DN == 16) ? 2 : 1;  // P^T buffers
+    static constexpr uint32_t col_o = 2 * DN;
+    static constexpr uint32_t cols = DN == 16 ? 64 : 128;
+};
+
+template <int NR, bool MAX>
+__device__ __forceinline__ float reduce_rows(const float (&v)[NR]) {
+    // reduce-scatter over the warp: row (lane >> (5 - log2 NR))'s result
+    const int lane = threadIdx.x & 31;
+    float a[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) a[i] = v[i];
+    int o = 16;
+#pragma unroll
+    for (int h = NR / 2; h >= 1; h /= 2, o /= 2) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float keep = up ? a[i + h] : a[i];
+            const float send = up ? a[i] : a[i + h];
+            const float got = __shfl_xor_sync(0xffffffffu, send, o);
+            a[i] = MAX ? fmaxf(keep, got) : keep + got;
+        }
+    }
+#pragma unroll
+    for (; o >= 1; o /= 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, a[0], o);
+        a[0] = MAX ? fmaxf(a[0], got) : a[0] + got;
+    }
+    return a[0];
+}
+
+template <typename T, int EB, int DN>
+__device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bars,
+                           const PagedStart* st, volatile int* abort) {
+    using S = Shape<EB, DN>;
+    const PagedAttendParams& a = p.a;
+    const int lane = threadIdx.x & 31;
+    PagedItem* items = reinterpret_cast<PagedItem*>(smem + p.off_item);
+    const int nkb = (a.D * EB + 127) / 128;
+    PagedWalk<kTS> w;
+    w.start(p, st);
+    const long long unit0 = w.at - w.tt;
+    PagedItem it;
+    int unit_tiles = 0;
+    bool more = w.next(p, it, unit_tiles);
+    if (lane == 0)
+        paged_record(p, more && !(it.flags & kItemBegins) ? &it : nullptr, unit0, unit_tiles, w.per);
+    for (int k = 0;; ++k) {
+        const int kb = k % p.ni;
+        if (k >= p.ni &&
+            !warp_wait(bars.item_empty(kb), static_cast<uint32_t>((k / p.ni - 1) & 1), abort))
+            return;
+        if (!more) {
+            if (lane == 0) items[kb].flags = kItemDone;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);
+            return;
+        }
+        unsigned char* sq = smem + p.off_q + kb * p.q_bytes;
+        RowData* rd = reinterpret_cast<RowData*>(sq + S::kParts * nkb * S::nblk);
+        const int R = it.S * a.G;
+        if (lane == 0) {
+            items[kb] = it;
+            *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 0;
+        }
+        {
+            const int r = it.r0 + lane;
+            const bool live = lane < p.RG && r < R;
+            rd->lim[lane] = live ? it.K - it.S + r / a.G : -1;
+            rd->slope[lane] = live && a.slopes ? a.slopes[it.hk * a.G + r % a.G] * kLog2e : 0.f;
+        }
+#pragma unroll 2
+        for (int r = 0; r < DN; ++r) {
+            const int rr = it.r0 + r;
+            const bool live = r < p.RG && rr < R;
+            const T* q = static_cast<const T*>(a.q) + (it.q0 + (live ? rr / a.G : 0)) * a.q_tok +
+                         (static_cast<int64_t>(it.hk) * a.G + (live ? rr % a.G : 0)) * a.q_head;
+            if (EB == 2) {
+                for (int c = lane; c < nkb * 8; c += 32) {  // 16-byte chunks
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (live && c * 8 < a.D) v = *reinterpret_cast<const uint4*>(q + c * 8);
+                    *reinterpret_cast<uint4*>(sq + (c >> 3) * S::nblk + r * 128 +
+                                              (((c & 7) ^ (r & 7)) << 4)) = v;
+                }
+                if (lane == 0) rd->mul[r] = a.scale;
+            } else {
+                float x[2][4];
+                float big = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int d = c * 128 + lane * 4;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
+                    if (live && d < a.D) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(q + d);
+                        const T* h = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[c][e] = Storage<T>::to_float(h[e]);
+                            if (fabsf(x[c][e]) < INFINITY)
+                                big = fmaxf(big, fabsf(x[c][e]));
+                            else
+                                x[c][e] = __uint_as_float(0x7fffffffu);  // no 8-bit infinity: NaN
+                        }
+                    }
+                }
+                big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+                // 2^e: the row's largest element then lies in [2^7, 2^8)
+                int e2 = 7 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
+                e2 = max(-120, min(120, e2));
+                const float f = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (c >= nkb) break;
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float u = x[c][e] * f, v = x[c][e + 1] * f;
+                        const uint32_t h2 = to_eight2<false>(u, v);
+                        const float2 hf = from_eight2<false>(h2);
+                        hi |= h2 << (8 * e);
+                        lo |= to_eight2<false>(u - hf.x, v - hf.y) << (8 * e);
+                    }
+                    const int o = c * S::nblk + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t*>(sq + o) = hi;
+                    *reinterpret_cast<uint32_t*>(sq + nkb * S::nblk + o) = lo;
+                }
+                if (lane == 0)
+                    rd->mul[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+            }
+        }
+        fence_async_shared();  // the query rows, for the tensor cores
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);
+        more = w.next(p, it, unit_tiles);
+    }
+}
+
+template <int EB>
+__device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars bars,
+                              volatile int* abort) {
+    const PagedAttendParams& a = p.a;
+    const int lane = threadIdx.x & 31;
+    const uint32_t stage0 = smem_addr(smem + p.off_stage);
+    StageScales* sc = reinterpret_cast<StageScales*>(smem + 1024);
+    const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
+    const int nkb = (a.D * EB + 127) / 128;
+    const int nvb = EB == 1 ? 1 : 2;  // value columns padded to 128: the boxes past them read zeros
+    int issued = 0;
+    Ring ring;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const int kb = k % p.ni;
+        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        const PagedItem it = items[kb];
+        if (it.flags & kItemDone) break;
+        for (int n = 0; n < it.nt; ++n) {
+            if (issued >= p.ns && !warp_wait(bars.empty(ring.s), ring.ph ^ 1u, abort)) {
+                ok = false;
+                break;
+            }
+            const uint32_t sK = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes;
+            const uint32_t sV = sK + static_cast<uint32_t>(nkb * kTS * 128);
+            if (!paged_load_tile<EB, kTS>(p, it, it.tile0 + n, sK, sV, nkb, nvb, sc + ring.s,
+                                          bars.full(ring.s)) &&
+                lane == 0) {
+                *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 1;
+                if (a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
+            }
+            ++issued;
+            ring.next(p.ns);
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bars.item_empty(kb), 1u);
+    }
+    // do not leave while issued copies may still write shared memory
+    if (lane == 0)
+        for (int q = issued > p.ns ? issued - p.ns : 0; q < issued; ++q)
+            mbar_drain(bars.full(q % p.ns), static_cast<uint32_t>((q / p.ns) & 1));
+}
+
+// One thread: S^T of every tile.
+template <typename T, int EB, int DN>
+__device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
+                         uint32_t tmem) {
+    using S = Shape<EB, DN>;
+    const PagedAttendParams& a = p.a;
+    const uint32_t stage0 = smem_addr(smem + p.off_stage);
+    const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
+    const int nkb = (a.D * EB + 127) / 128;
+    const int ksteps = (a.D * EB + 31) / 32;  // 32 bytes of a row per instruction
+    const uint32_t idesc = EB == 1 ? mma_idesc_f8(kTS, DN, a.e5m2, false, false, false)
+                                   : mma_idesc_f16(kTS, DN, std::is_same<T, __nv_bfloat16>::value,
+                                                   false, false);
+    Ring ring;
+    int c = 0;  // tiles so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const int kb = k % p.ni;
+        if (!mbar_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (items[kb].flags & kItemDone) break;
+        const int nt = items[kb].nt;
+        const uint32_t sQ = smem_addr(smem + p.off_q + kb * p.q_bytes);
+        for (int n = 0; n < nt; ++n, ++c) {
+            const int sb = c & 1;
+            if (!mbar_wait(bars.full(ring.s), ring.ph, abort) ||
+                (c >= 2 && !mbar_wait(bars.s_free(sb), static_cast<uint32_t>((c / 2 - 1) & 1), abort))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t sK = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes;
+            for (int part = 0; part < S::kParts; ++part)
+                for (int i = 0; i < ksteps; ++i) {
+                    const uint64_t da = smem_desc_sw128(sK + (i >> 2) * kTS * 128 + (i & 3) * 32, 16, 1024);
+                    const uint64_t db = smem_desc_sw128(
+                        sQ + (part * nkb + (i >> 2)) * S::nblk + (i & 3) * 32, 16, 1024);
+                    if (EB == 1)
+                        tc_mma_f8(tmem + sb * DN, da, db, idesc, (part | i) != 0);
+                    else
+                        tc_mma(tmem + sb * DN, da, db, idesc, i != 0);
+                }
+            tc_commit(bars.s_ready(sb));
+            ring.next(p.ns);
+        }
+        if (ok) tc_commit(bars.item_empty(kb));  // once the products have read the query rows
+    }
+    tc_commit(bars.drained());
+    volatile int never = 0;
+    mbar_wait(bars.drained(), 0u, &never);
+}
+
+// One thread: O^T += V^T P^T of every tile; releases the stages.
+template <typename T, int EB, int DN>
+__device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
+                          uint32_t tmem) {
+    using S = Shape<EB, DN>;
+    const PagedAttendParams& a = p.a;
+    const uint32_t stage0 = smem_addr(smem + p.off_stage);
+    const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
+    const int nkb = (a.D * EB + 127) / 128;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    Ring ring;
+    int c = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const int kb = k % p.ni;
+        if (!mbar_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (items[kb].flags & kItemDone) break;
+        const int nt = items[kb].nt;
+        for (int n = 0; n < nt; ++n, ++c) {
+            const int pb = c % S::npt;
+            if (!mbar_wait(bars.full(ring.s), ring.ph, abort) ||
+                !mbar_wait(bars.p_ready(pb), static_cast<uint32_t>((c / S::npt) & 1), abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t sV = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes +
+                                static_cast<uint32_t>(nkb * kTS * 128);
+            const uint32_t sP = smem_addr(smem + p.off_p) + pb * S::pbytes;
+            if (EB == 1) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)  // e4m3, then what it leaves in e5m2
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)       // 32 slots per instruction
+                        tc_mma_f8(tmem + S::col_o, smem_desc_sw128(sV + i * 32 * 128, 16, 1024),
+                                  smem_desc_sw128(sP + part * S::nblk + i * 32, 16, 1024),
+                                  mma_idesc_f8(128, DN, a.e5m2, part != 0, true, false),
+                                  n != 0 || (part | i) != 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)           // 16 slots per instruction
+                    tc_mma(tmem + S::col_o, smem_desc_sw128(sV + i * 16 * 128, kTS * 128, 1024),
+                           smem_desc_sw128(sP + (i >> 2) * S::nblk + (i & 3) * 32, 16, 1024),
+                           mma_idesc_f16(128, DN, kBf16, false, true), (n | i) != 0);
+            }
+            tc_commit(bars.o_done(pb));
+            tc_commit(bars.empty(ring.s));
+            ring.next(p.ns);
+        }
+        if (ok) mbar_arrive(bars.item_empty(kb), 1u);
+    }
+    tc_commit(bars.drained());
+    volatile int never = 0;
+    mbar_wait(bars.drained(), 0u, &never);
+}
+
+// 32-bit words whose 8- or 16-bit fields that hold an infinity or NaN are cleared.
+template <int EB, typename T>
+__device__ __forceinline__ uint32_t clear_odd(uint32_t w, bool e5m2) {
+    uint32_t keep = 0xffffffffu;
+    if (EB == 2) {
+        const uint32_t inf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+        if ((w & 0x7fffu) >= inf) keep &= 0xffff0000u;
+        if (((w >> 16) & 0x7fffu) >= inf) keep &= 0x0000ffffu;
+    } else {
+        const uint32_t inf = e5m2 ? 0x7cu : 0x7fu;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (((w >> (8 * i)) & 0x7fu) >= inf) keep &= ~(0xffu << (8 * i));
+    }
+    return w & keep;
+}
+
+template <typename T, int EB, int NR, bool MOD>
+__device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars bars,
+                              volatile int* abort, uint32_t tmem, const PagedStart* st) {
+    constexpr int DN = NR <= 16 ? 16 : 32;
+    using S = Shape<EB, DN>;
+    using St = Storage<T>;
+    const PagedAttendParams& a = p.a;
+    const int t = threadIdx.x & 127;  // slot of the tile; value column of O^T
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
+    const StageScales* scales = reinterpret_cast<const StageScales*>(smem + 1024);
+    // exchange: values [2][NR][4], flags [2][4]
+    float* xval = reinterpret_cast<float*>(smem + p.off_x);
+    int* xflag = reinterpret_cast<int*>(smem + p.off_x + 2 * NR * 4 * 4);
+    unsigned char* pt = smem + p.off_p;
+    const int nkb = (a.D * EB + 127) / 128;
+    constexpr int nvb = EB == 1 ? 1 : 2;
+    constexpr int kGroup = 32 / NR;  // lanes that end a reduction with one row
+    const int box = 31 - __clz(p.hh);
+    Ring ring;
+    int c = 0;        // tiles so far
+    uint32_t rv = 0;  // meetings so far
+    float mref[NR], lsum[NR];
+
+    // The 4 warps meet (a bounded wait, unlike bar.sync); what each wrote to
+    // exchange buffer rv % 2 before is visible to all after.
+    auto meet = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.meet(), 1u);
+        const bool ok = warp_wait(bars.meet(), rv & 1u, abort);
+        ++rv;
+        return ok;
+    };
+    auto wait_pv = [&](int i) -> bool {  // product i has finished
+        return warp_wait(bars.o_done(i % S::npt), static_cast<uint32_t>((i / S::npt) & 1), abort);
+    };
+    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+    const float cap_out = a.softcap * kLog2e;
+
+    for (int k = 0;; ++k) {
+        const int kb = k % p.ni;
+        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) return;
+        const PagedItem it = items[kb];
+        if (it.flags & kItemDone) return;
+        const RowData* rd = reinterpret_cast<const RowData*>(smem + p.off_q + kb * p.q_bytes +
+                                                             S::kParts * nkb * S::nblk);
+        // set behind this run's first meeting, read behind its last
+        volatile int* odd = reinterpret_cast<volatile int*>(smem + kOdd + 4 * (k & 1));
+        if (threadIdx.x == 0) *odd = 0;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            mref[r] = -INFINITY;
+            lsum[r] = 0.f;
+        }
+        for (int n = 0; n < it.nt; ++n, ++c) {
+            const int sb = c & 1;
+            if (!warp_wait(bars.full(ring.s), ring.ph, abort) ||
+                !warp_wait(bars.s_ready(sb), static_cast<uint32_t>((c / 2) & 1), abort))
+                return;
+            tc_fence_after();
+            float sv[NR];
+            if constexpr (NR == 32)
+                tmem_ld32(trow + sb * DN, sv);
+            else
+                tmem_ldn<NR>(trow + sb * DN, sv);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.s_free(sb), 1u);
+            float ksc = 1.f, ivs = 1.f, lv = 0.f;  // key scale, 1 / value scale, its log2
+            if (EB == 1) {
+                const float2 kv = scales[ring.s].kv[t >> box];
+                ksc = kv.x;
+                ivs = 1.f / kv.y;
+                lv = __log2f(kv.y);
+            }
+            const int j0 = (it.tile0 + n) * kTS, j = j0 + t;
+            // a tile with a slot that some row does not see
+            const bool edge = j0 + kTS - 1 > it.first || (a.window > 0 && j0 <= it.last - a.window);
+            if (!MOD) ksc *= kLog2e;
+            uint32_t seen = 0xffffffffu;
+            if (edge) {
+                seen = 0u;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int lim = rd->lim[r];
+                    if (j <= lim && (a.window == 0 || j > lim - a.window)) seen |= 1u << r;
+                }
+            }
+            if (seen == 0u) ivs = 0.f;  // its box may not have been read
+            bool need = false;
+#pragma unroll
+            for (int r = 0; r < NR; r += 4) {
+                const float4 m4 = *reinterpret_cast<const float4*>(rd->mul + r);
+                const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float s = sv[r + e] * (m[e] * ksc);
+                    if (MOD) {
+                        if (a.softcap > 0.f) {
+                            // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+                            const float ex = fast_exp2(s * cap_in);
+                            s = cap_out - __fdividef(2.f * cap_out, 1.f + ex);
+                            if (!(ex < INFINITY)) s = ex == ex ? cap_out : ex;
+                        } else {
+                            s *= kLog2e;
+                        }
+                        s -= rd->slope[r + e] * static_cast<float>(rd->lim[r + e] - j);
+                    }
+                    s += lv;
+                    if (!((seen >> (r + e)) & 1u)) s = -INFINITY;
+                    sv[r + e] = s;
+                    need |= s > mref[r + e] + Threshold<EB>::v;
+                }
+            }
+            // the references are raised for the whole tile or not at all
+            const uint32_t bf = rv & 1u;
+            const int wneed = __any_sync(0xffffffffu, need);
+            if (lane == 0) xflag[bf * 4 + warp] = wneed;
+            if (!meet()) return;
+            const int4 fl = *reinterpret_cast<const int4*>(xflag + bf * 4);
+            bool rescale = false;
+            float corr[NR];
+            if (fl.x | fl.y | fl.z | fl.w) {
+                const uint32_t bm = rv & 1u;
+                const float mine = reduce_rows<NR, true>(sv);
+                if ((lane & (kGroup - 1)) == 0) xval[(bm * NR + lane / kGroup) * 4 + warp] = mine;
+                if (!meet()) return;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(xval + (bm * NR + r) * 4);
+                    const float top = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
+                    corr[r] = 1.f;
+                    if (top > mref[r] + Threshold<EB>::v) {
+                        if (mref[r] != -INFINITY) {
+                            corr[r] = fast_exp2(mref[r] - top);
+                            rescale = true;
+                        }
+                        lsum[r] *= corr[r];
+                        mref[r] = top;
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                // a row that saw nothing yet has no reference: every slot of it is masked
+                sv[r] = sv[r] == -INFINITY ? 0.f : fast_exp2(sv[r] - mref[r] + kOffset);
+                lsum[r] = EB == 1 ? fmaf(sv[r], ivs, lsum[r]) : lsum[r] + sv[r];
+            }
+            if (c >= S::npt && !wait_pv(c - S::npt)) return;
+            unsigned char* pb = pt + (c % S::npt) * S::pbytes;
+            if (EB == 1) {
+#pragma unroll
+                for (int r = 0; r < NR; r += 2) {
+                    const uint32_t hi = to_eight2<false>(sv[r], sv[r + 1]);
+                    const float2 hf = from_eight2<false>(hi);
+                    const uint32_t lo = to_eight2<true>(sv[r] - hf.x, sv[r + 1] - hf.y);
+                    unsigned char* o0 = pb + r * 128 + (((t >> 4) ^ (r & 7)) << 4) + (t & 15);
+                    unsigned char* o1 = pb + (r + 1) * 128 + (((t >> 4) ^ ((r + 1) & 7)) << 4) + (t & 15);
+                    o0[0] = static_cast<unsigned char>(hi);
+                    o1[0] = static_cast<unsigned char>(hi >> 8);
+                    o0[S::nblk] = static_cast<unsigned char>(lo);
+                    o1[S::nblk] = static_cast<unsigned char>(lo >> 8);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    *reinterpret_cast<T*>(pb + (t >> 6) * S::nblk + r * 128 +
+                                          ((((t & 63) >> 3) ^ (r & 7)) << 4) + (t & 7) * 2) =
+                        St::from_float(sv[r]);
+            }
+            if (edge) {
+                unsigned char* vrow = smem + p.off_stage + static_cast<int64_t>(ring.s) * p.stage_bytes +
+                                      nkb * kTS * 128 + t * 128;
+                const bool some = j <= it.last && j >= it.lo;
+                const bool all = j <= it.first && (a.window == 0 || j > it.last - a.window);
+                if (!some) {
+                    for (int b = 0; b < nvb; ++b)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4*>(vrow + b * kTS * 128 + i * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                } else if (!all) {
+                    for (int b = 0; b < nvb; ++b)
+                        for (int i = 0; i < 32; ++i) {
+                            uint32_t* w = reinterpret_cast<uint32_t*>(vrow + b * kTS * 128) +
+                                          ((i + lane) & 31);
+                            const uint32_t v = *w, u = clear_odd<EB, T>(v, a.e5m2);
+                            if (u != v) {
+                                *w = u;
+                                *odd = 1;
+                            }
+                        }
+                }
+            }
+            if (rescale && n > 0) {
+                // O^T is at rest: the previous product has finished, this tile's
+                // waits for p_ready
+                if (!wait_pv(c - 1)) return;
+                tc_fence_after();
+                float ov[NR];
+                if constexpr (NR == 32)
+                    tmem_ld32(trow + S::col_o, ov);
+                else
+                    tmem_ldn<NR>(trow + S::col_o, ov);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) ov[r] *= corr[r];
+                if constexpr (NR == 32)
+                    tmem_st32(trow + S::col_o, ov);
+                else
+                    tmem_stn<NR>(trow + S::col_o, ov);
+            }
+            fence_async_shared();  // the weights and cleared value rows, for the tensor cores
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.p_ready(c % S::npt), 1u);
+            ring.next(p.ns);
+        }
+        // the run's end: O^T column r is row r's weighted values
+        if (!wait_pv(c - 1)) return;
+        tc_fence_after();
+        float ov[NR];
+        if constexpr (NR == 32)
+            tmem_ld32(trow + S::col_o, ov);
+        else
+            tmem_ldn<NR>(trow + S::col_o, ov);
+        tc_fence_before();
+        const uint32_t bm = rv & 1u;
+        const float mine = reduce_rows<NR, false>(lsum);
+        if ((lane & (kGroup - 1)) == 0) xval[(bm * NR + lane / kGroup) * 4 + warp] = mine;
+        if (!meet()) return;
+        if (*odd && t < a.Dv) {  // what was cleared: from memory, into the rows that see it
+            const int j1 = min(it.last, (it.tile0 + it.nt) * kTS - 1);
+            for (int j = max(it.lo, it.tile0 * kTS); j <= j1; ++j) {
+                if (j <= it.first && (a.window == 0 || j > it.last - a.window)) {
+                    // seen by all: to the next slot that is not (behind the first row, if any)
+                    j = max(j, it.first);
+                    continue;
+                }
+                const int id = a.table[it.b * a.max_blocks + j / a.bs];
+                if (id < 0 || id >= a.num_blocks) continue;
+                const int64_t e = ((static_cast<int64_t>(id) * a.Hk + it.hk) * a.bs + j % a.bs) * a.Dv + t;
+                const float v = EB == 1 ? from_eight(static_cast<const uint8_t*>(a.vp)[e], a.e5m2)
+                                        : St::to_float(static_cast<const T*>(a.vp)[e]);
+                if (fabsf(v) < INFINITY) continue;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int lim = rd->lim[r];
+                    if (j <= lim && (a.window == 0 || j > lim - a.window)) ov[r] += v;
+                }
+            }
+        }
+        const bool bad = *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) != 0;
+        const bool whole = (it.flags & kItemBegins) && (it.flags & kItemEnds);
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + ((it.flags & kItemBegins) ? 1 : 0);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int lim = rd->lim[r];
+            if (lim < 0) continue;
+            const float4 q4 = *reinterpret_cast<const float4*>(xval + (bm * NR + r) * 4);
+            const float l = (q4.x + q4.y) + (q4.z + q4.w);
+            if (whole) {
+                const int rr = it.r0 + r;
+                const int64_t row = static_cast<int64_t>(it.q0 + rr / a.G) * a.Hq + it.hk * a.G + rr % a.G;
+                if (t < a.Dv)
+                    static_cast<T*>(a.out)[row * a.Dv + t] =
+                        St::from_float(bad ? 0.f : __fdiv_rn(ov[r], l));
+            } else {
+                if (t < a.Dv) p.part_acc[(slot * p.RG + r) * a.Dv + t] = ov[r];
+                if (t == r) {
+                    p.part_ml[2 * (slot * p.RG + r)] = mref[r];
+                    p.part_ml[2 * (slot * p.RG + r) + 1] = bad ? -1.f : l;
+                }
+            }
+        }
+        // the run's row data and flags are read; the next meeting or product
+        // does not reuse them before every warp has arrived here
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.item_empty(kb), 1u);
+    }
+}
+
+template <typename T, int EB, int NR, bool MOD>
+__global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
+    paged_decode_kernel(const __grid_constant__ PagedTcParams p) {
+    constexpr int DN = NR <= 16 ? 16 : 32;
+    using S = Shape<EB, DN>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const Bars bars{smem_addr(smem)};
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + kAbort);
+    PagedStart* st = reinterpret_cast<PagedStart*>(smem + 512);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.ns; ++s) {
+            mbar_init(bars.full(s), 1u);
+            mbar_init(bars.empty(s), 1u);
+        }
+        for (int k = 0; k < p.ni; ++k) {
+            mbar_init(bars.item_full(k), 1u);
+            mbar_init(bars.item_empty(k), 3u + 4u);  // producer, both issuers, softmax warps
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bars.s_ready(b), 1u);
+            mbar_init(bars.s_free(b), 4u);
+            mbar_init(bars.p_ready(b), 4u);
+            mbar_init(bars.o_done(b), 1u);
+        }
+        mbar_init(bars.meet(), 4u);
+        mbar_init(bars.drained(), 2u);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    // weights of rows past the unit's stay zero: clear the buffers once
+    for (int i = threadIdx.x; i < S::npt * S::pbytes / 16; i += kThreads)
+        reinterpret_cast<uint4*>(smem + p.off_p)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_shared();
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(smem + kTmemSlot), S::cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    paged_plan<kTS, kThreads>(p, st);  // with block barriers
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemSlot);
+    launch_dependents();
+
+    if (warp < 4) {
+        softmax_warps<T, EB, NR, MOD>(p, smem, bars, abort, tmem, st);
+    } else if (warp == kMmaWarp) {
+        if ((threadIdx.x & 31) == 0) s_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
+    } else if (warp == kPvWarp) {
+        if ((threadIdx.x & 31) == 0) pv_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
+    } else if (warp == kProdWarp) {
+        producer_warp<EB>(p, smem, bars, abort);
+    } else {
+        sched_warp<T, EB, DN>(p, smem, bars, st, abort);
+    }
+    tc_fence_before();
+    __syncthreads();  // every thread reaches this exactly once: all waits are bounded
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::cols);
+    }
+    if (threadIdx.x == 0 && *abort && p.a.status) atomicOr(p.a.status, KVC_DEV_TIMEOUT);
+    paged_zero_invalid<T, kThreads>(p);
+}
+
+// Block (c, y): the unit whose second block is c, rows y, y + gridDim.y, ...
+// 8 warps take the partials in turn, a lane four value columns.
+template <typename T>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedTcParams p) {
+    __shared__ float sh[8][128];
+    __shared__ float shl[8];
+    grid_dependency_wait();
+    const PagedAttendParams& a = p.a;
+    const PagedRec rec = p.rec[blockIdx.x];
+    if (!rec.valid || static_cast<int>(blockIdx.x) != rec.c0 + 1) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = rec.c1 - rec.c0 + 1;
+    auto slot = [&](int k) -> int64_t {
+        return 2 * static_cast<int64_t>(rec.c0 + k) + (k == 0 ? 1 : 0);
+    };
+    for (int r = blockIdx.y; r < rec.rows; r += gridDim.y) {
+        float m = -INFINITY;
+        int bad = 0;
+        for (int k = lane; k < n; k += 32) {
+            const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[slot(k) * p.RG + r];
+            if (ml.y < 0.f) bad = 1;
+            if (ml.y != 0.f) m = fmaxf(m, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        bad = __any_sync(0xffffffffu, bad);
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = warp; k < n; k += 8) {
+            const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[slot(k) * p.RG + r];
+            const float f = ml.y == 0.f ? 0.f : ml.x == m ? 1.f : fast_exp2(ml.x - m);
+            const float* src = p.part_acc + (slot(k) * p.RG + r) * a.Dv + 4 * lane;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (4 * lane < a.Dv) v = *reinterpret_cast<const float4*>(src);
+            if (ml.y != 0.f) {
+                l = fmaf(ml.y, f, l);
+                acc.x = fmaf(v.x, f, acc.x);
+                acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z);
+                acc.w = fmaf(v.w, f, acc.w);
+            }
+        }
+        reinterpret_cast<float4*>(sh[warp])[lane] = acc;
+        if (lane == 0) shl[warp] = l;
+        __syncthreads();
+        if (threadIdx.x < a.Dv) {
+            float o = 0.f, ll = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                o += sh[w][threadIdx.x];
+                ll += shl[w];
+            }
+            const int rr = rec.r0 + r;
+            const int64_t row = static_cast<int64_t>(rec.q0 + rr / a.G) * a.Hq + rec.hk * a.G + rr % a.G;
+            static_cast<T*>(a.out)[row * a.Dv + threadIdx.x] =
+                Storage<T>::from_float(bad ? 0.f : __fdiv_rn(o, ll));
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int EB, int NR, bool MOD>
+cudaError_t launch_t(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
+    auto kern = paged_decode_kernel<T, EB, NR, MOD>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(p.ctas), kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+template <typename T, int EB>
+cudaError_t launch_eb(const PagedTcParams& p, int nr, size_t smem, cudaStream_t stream) {
+    const bool mod = p.a.softcap > 0.f || p.a.slopes;
+    switch (nr) {
+        case 4: return mod ? launch_t<T, EB, 4, true>(p, smem, stream) : launch_t<T, EB, 4, false>(p, smem, stream);
+        case 8: return mod ? launch_t<T, EB, 8, true>(p, smem, stream) : launch_t<T, EB, 8, false>(p, smem, stream);
+        case 16: return mod ? launch_t<T, EB, 16, true>(p, smem, stream) : launch_t<T, EB, 16, false>(p, smem, stream);
+        default: return mod ? launch_t<T, EB, 32, true>(p, smem, stream) : launch_t<T, EB, 32, false>(p, smem, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const PagedTcParams& p, int dtype, int pool_dtype, int nr,
+                                size_t smem, cudaStream_t stream) {
+    if (pool_dtype == dtype)
+        return dtype == KVC_BF16 ? launch_eb<__nv_bfloat16, 2>(p, nr, smem, stream)
+                                 : launch_eb<__half, 2>(p, nr, smem, stream);
+    return dtype == KVC_BF16 ? launch_eb<__nv_bfloat16, 1>(p, nr, smem, stream)
+                             : launch_eb<__half, 1>(p, nr, smem, stream);
+}
+
+cudaError_t launch_paged_merge(const PagedTcParams& p, int dtype, cudaStream_t stream) {
+    if (p.ctas < 2) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(std::min(p.RG, 8)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return dtype == KVC_BF16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, p)
+                             : cudaLaunchKernelEx(&cfg, paged_merge_kernel<__half>, p);
+}
+
+}  // namespace kvc

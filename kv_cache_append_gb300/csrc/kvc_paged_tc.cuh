@@ -1,0 +1,307 @@
+// kvc_paged_tc.cuh -- what the tensor-core kernels of the paged attention
+// share (kvc_paged_decode.cu, kvc_paged_rows.cu): the even split of the work, the
+// tile producer and the tensor-core forms for 8-bit operands.
+//
+// Work. A unit is (sequence, group of up to RG query rows, KV head); rows r =
+// t G + g of a KV head are grouped in order. Its tiles are the runs of TS slots
+// (aligned to TS) from its first visible slot to its last. All units' tiles in
+// order (sequence, group, head) are one list; block c of the grid takes tiles [c per,
+// (c + 1) per). Every block computes the list's length itself from cu_seqlens
+// and seqlens_k (one pass over B sequences), so a call is one launch, whatever the
+// lengths, and no block has more than one tile more than another. A unit that lies
+// within one block is finished there; of a unit cut between blocks each block
+// leaves a partial (at most two per block: the tail of a unit in slot 0, the
+// head of one in slot 1), which paged_merge_kernel joins.
+#pragma once
+
+#include <cuda.h>
+
+#include "kvc_launch.h"
+#include "kvc_paged.cuh"
+#include "kvc_pipeline.cuh"
+#include "kvc_tcgen05.cuh"
+
+namespace kvc {
+
+// D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4: 8-bit operands (each of its
+// own format), fp32 accumulate, 32 elements of K per instruction.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// Instruction descriptor of a kind::f8f6f4 product with fp32 accumulation.
+__device__ __forceinline__ uint32_t mma_idesc_f8(int M, int N, bool a_e5m2, bool b_e5m2,
+                                                 bool a_mn_major, bool b_mn_major) {
+    return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) |
+           ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The slots that query rows [r0, r0 + RG) of a sequence see, and their tiles.
+struct PagedGroup {
+    int first, last;  // positions of the group's first and last row
+    int lo;           // first slot any of them sees (the last is `last`)
+    int tile0, nt;
+};
+template <int TS>
+__device__ __forceinline__ PagedGroup paged_group(const PagedAttendParams& a, int RG, int S, int K,
+                                                  int i) {
+    PagedGroup g;
+    const int R = S * a.G, r0 = i * RG;
+    g.first = K - S + r0 / a.G;
+    g.last = K - S + (min(R, r0 + RG) - 1) / a.G;
+    g.lo = a.window > 0 ? max(0, g.first - a.window + 1) : 0;
+    g.tile0 = g.lo / TS;
+    g.nt = g.last / TS - g.tile0 + 1;
+    return g;
+}
+__device__ __forceinline__ int paged_groups(const PagedAttendParams& a, int RG, int S) {
+    return (S * a.G + RG - 1) / RG;
+}
+
+// A run of tiles of one unit, as the scheduling warp hands it to the others.
+struct PagedItem {
+    int b, q0, S, K;
+    int r0, hk;          // the group's first row, KV head
+    int first, last, lo; // as PagedGroup
+    int tile0, nt;       // the run
+    int flags;
+};
+constexpr int kItemBegins = 1;  // the run starts the unit
+constexpr int kItemEnds = 2;    // the run ends the unit
+constexpr int kItemDone = 4;    // no more runs
+
+// Where a block's run of the tile list starts, found by all threads of it.
+struct PagedStart {
+    long long total, per;
+    int b;          // sequence of the first tile
+    long long off;  // its tile within the sequence
+    long long sums[32];
+};
+
+template <int TS>
+__device__ __forceinline__ long long paged_seq_tiles(const PagedTcParams& p, int64_t b) {
+    const PagedAttendParams& a = p.a;
+    const PagedSeq s = paged_seq(a.cu, a.kl, b, a.total_q, a.max_q, a.M);
+    if (!s.ok || s.S == 0) return 0;
+    long long n = 0;
+    const int ng = paged_groups(a, p.RG, s.S);
+    for (int i = 0; i < ng; ++i) n += paged_group<TS>(a, p.RG, s.S, s.K, i).nt;
+    return n * a.Hk;
+}
+
+// All threads; ends with a block barrier.
+template <int TS, int THREADS>
+__device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* st) {
+    const int64_t B = p.a.B;
+    const int64_t per_thread = (B + THREADS - 1) / THREADS;
+    const int64_t b0 = min(B, threadIdx.x * per_thread), b1 = min(B, b0 + per_thread);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long mine = 0;
+    for (int64_t b = b0; b < b1; ++b) mine += paged_seq_tiles<TS>(p, b);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) st->sums[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const long long v = st->sums[w];
+        if (w < warp) before += v;
+        total += v;
+    }
+    const long long per = (total + p.ctas - 1) / p.ctas;
+    const long long at = static_cast<long long>(blockIdx.x) * per;
+    long long cur = before + incl - mine;
+    if (threadIdx.x == 0) {
+        st->total = total;
+        st->per = per;
+    }
+    if (at >= cur && at < cur + mine) {
+        for (int64_t b = b0; b < b1; ++b) {
+            const long long n = paged_seq_tiles<TS>(p, b);
+            if (at < cur + n) {
+                st->b = static_cast<int>(b);
+                st->off = at - cur;
+                break;
+            }
+            cur += n;
+        }
+    }
+    __syncthreads();
+}
+
+// Rows of sequences outside the contract are zero; their count is not large,
+// so block c sees to sequences c, c + grid, ...
+template <typename T, int THREADS>
+__device__ __forceinline__ void paged_zero_invalid(const PagedTcParams& p) {
+    const PagedAttendParams& a = p.a;
+    for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const PagedSeq s = paged_seq(a.cu, a.kl, b, a.total_q, a.max_q, a.M);
+        if (s.ok) continue;
+        if (threadIdx.x == 0 && a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
+        const int64_t n = static_cast<int64_t>(s.S) * a.Hq * a.Dv;
+        T* o = static_cast<T*>(a.out) + static_cast<int64_t>(s.q0) * a.Hq * a.Dv;
+        for (int64_t i = threadIdx.x; i < n; i += THREADS) o[i] = Storage<T>::from_float(0.f);
+    }
+}
+
+// The scheduling warp's walk over its block's runs (all lanes alike).
+template <int TS>
+struct PagedWalk {
+    long long left = 0, at = 0;  // tiles to hand out, the list index of the next
+    long long per = 1;
+    int b = 0, i = 0, hk = 0, tt = 0;  // next tile: sequence, group, head, tile of the unit
+    PagedSeq s{};
+    int ng = 0;
+
+    __device__ void load(const PagedTcParams& p) {
+        s = paged_seq(p.a.cu, p.a.kl, b, p.a.total_q, p.a.max_q, p.a.M);
+        ng = s.ok ? paged_groups(p.a, p.RG, s.S) : 0;
+    }
+    __device__ void start(const PagedTcParams& p, const PagedStart* st) {
+        per = st->per;
+        at = static_cast<long long>(blockIdx.x) * per;
+        left = min(per, st->total - at);
+        if (left <= 0) return;
+        b = st->b;
+        load(p);
+        // the group of tile `off`: 32 groups at a time
+        long long off = st->off;
+        const int lane = threadIdx.x & 31;
+        for (i = 0;; i += 32) {
+            long long n = 0;
+            if (i + lane < ng)
+                n = static_cast<long long>(paged_group<TS>(p.a, p.RG, s.S, s.K, i + lane).nt) * p.a.Hk;
+            long long incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const uint32_t in = __ballot_sync(0xffffffffu, off < incl);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                off -= __shfl_sync(0xffffffffu, incl - n, l);
+                i += l;
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, incl, 31);
+            if (i + 32 >= ng) {  // not reached: off lies within the sequence
+                left = 0;
+                return;
+            }
+        }
+        const int n = paged_group<TS>(p.a, p.RG, s.S, s.K, i).nt;
+        hk = static_cast<int>(off / n);
+        tt = static_cast<int>(off - static_cast<long long>(hk) * n);
+    }
+    // The next run into `it`; false at the end.
+    __device__ bool next(const PagedTcParams& p, PagedItem& it, int& unit_tiles) {
+        if (left <= 0) return false;
+        while (ng == 0 || i >= ng) {
+            ++b;
+            if (b >= p.a.B) return false;
+            i = 0;
+            load(p);
+        }
+        const PagedGroup g = paged_group<TS>(p.a, p.RG, s.S, s.K, i);
+        const int take = static_cast<int>(min(static_cast<long long>(g.nt - tt), left));
+        it.b = b; it.q0 = s.q0; it.S = s.S; it.K = s.K;
+        it.r0 = i * p.RG; it.hk = hk;
+        it.first = g.first; it.last = g.last; it.lo = g.lo;
+        it.tile0 = g.tile0 + tt; it.nt = take;
+        it.flags = (tt == 0 ? kItemBegins : 0) | (tt + take == g.nt ? kItemEnds : 0);
+        unit_tiles = g.nt;
+        left -= take;
+        at += take;
+        tt += take;
+        if (tt == g.nt) {
+            tt = 0;
+            if (++hk == p.a.Hk) {
+                hk = 0;
+                ++i;
+            }
+        }
+        return true;
+    }
+};
+
+// The record of a block whose first run continues a unit: which unit, and the
+// blocks it lies in. Written for every block at every call.
+__device__ __forceinline__ void paged_record(const PagedTcParams& p, const PagedItem* it,
+                                             long long unit_start, int unit_tiles, long long per) {
+    PagedRec r{};
+    if (it) {
+        r.valid = 1;
+        r.q0 = it->q0; r.r0 = it->r0; r.hk = it->hk;
+        r.rows = min(p.RG, it->S * p.a.G - it->r0);
+        r.c0 = static_cast<int>(unit_start / per);
+        r.c1 = static_cast<int>((unit_start + unit_tiles - 1) / per);
+    }
+    p.rec[blockIdx.x] = r;
+}
+
+// Per stage: the key and value scale of each box of the tile.
+constexpr int kMaxBoxes = 16;
+struct StageScales {
+    float2 kv[kMaxBoxes];
+};
+
+// One tile's boxes (rows of one pool block each), by a whole warp: those
+// holding a visible slot. Returns false when a block id lies outside the pool
+// (block 0 is read instead).
+template <int EB, int TS>
+__device__ __forceinline__ bool paged_load_tile(const PagedTcParams& p, const PagedItem& it, int tile,
+                                                uint32_t sK, uint32_t sV, int nkb, int nvb,
+                                                StageScales* sc, uint32_t full) {
+    constexpr int kElems = 128 / EB;  // elements of a 128-byte column block
+    const PagedAttendParams& a = p.a;
+    const int lane = threadIdx.x & 31;
+    const int j0 = tile * TS, hh = p.hh;
+    const int pa = max(0, it.lo - j0) / hh, pb = (min(TS, it.last + 1 - j0) + hh - 1) / hh;
+    int id = 0, y = 0;
+    bool bad = false;
+    if (lane >= pa && lane < pb) {
+        const int slot = j0 + lane * hh, blk = slot / a.bs;
+        y = slot - blk * a.bs;
+        id = a.table[it.b * a.max_blocks + blk];
+        if (id < 0 || id >= a.num_blocks) {
+            bad = true;
+            id = 0;
+        }
+        if (EB == 1) {
+            const int64_t u = static_cast<int64_t>(id) * a.Hk + it.hk;
+            sc->kv[lane] = make_float2(a.ks[u], a.vs[u]);
+        }
+    }
+    __syncwarp();  // the scales are written before lane 0's arrive publishes the stage
+    const int nb = nkb + nvb, n = (pb - pa) * nb;
+    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * hh * 128));
+    __syncwarp();
+    const int z0 = id * a.Hk + it.hk;
+    for (int base = 0; base < n; base += 32) {
+        const int l = base + lane, c = pa + l / nb, k = l % nb;
+        const int z = __shfl_sync(0xffffffffu, z0, c & 31), yy = __shfl_sync(0xffffffffu, y, c & 31);
+        if (l < n) {
+            const uint32_t o = static_cast<uint32_t>(c * hh * 128);
+            if (k < nkb)
+                tma_load_3d(sK + k * TS * 128 + o, &p.tk, kElems * k, yy, z, full);
+            else
+                tma_load_3d(sV + (k - nkb) * TS * 128 + o, &p.tv, kElems * (k - nkb), yy, z, full);
+        }
+    }
+    return !__any_sync(0xffffffffu, bad);
+}
+
+}  // namespace kvc
