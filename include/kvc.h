@@ -418,9 +418,10 @@ KVC_API int kvc_attend_paged(const kvc_paged_dims *dims, const int64_t *q_stride
 
 /*
  * The kernel kvc_attend_paged takes for these sizes with 16-byte aligned pools
- * and queries: "decode" (tensor cores: at most 32 query rows max_q * Hq / Hk of a
- * KV head; 16-bit queries, rows of whole 16-byte words, D <= 256, Dv <= 128,
- * block_size a multiple of 8) or "cores" (CUDA cores: any size). Static text, or
+ * and queries: "decode" or "rows" (tensor cores, for at most 32 query rows
+ * max_q * Hq / Hk of a KV head, or more; 16-bit queries, pool rows of whole
+ * 16-byte words, D <= 256, Dv <= 128, block_size a multiple of 8), or "cores"
+ * (CUDA cores: any size). Static text, or
  * NULL for invalid dims. With an 8-bit pool the tensor-core kernels take a query
  * element as the sum of two e4m3 values (off by at most 2^-8 of it, or 2^-18 of
  * the row's largest) and a softmax weight as e4m3 + e5m2 (2^-7); with 16-bit

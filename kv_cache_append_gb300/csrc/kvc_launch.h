@@ -224,7 +224,8 @@ struct PagedTcParams {
     int RG;            // query rows of a unit
     int ctas;          // blocks of the grid
     int hh;            // slots of a box: the largest power of two up to 128 dividing block_size
-    int ns, ni;        // stages, item (and query) buffers
+    int ns, ni;        // stages (rows kernel: of keys), item and query buffers
+    int nv;            // rows kernel: stages of values
     int off_item, off_q, off_x, off_p, off_stage;  // shared memory
     int q_bytes, stage_bytes;
     float* part_ml;    // [2 ctas][RG][2]
@@ -234,6 +235,9 @@ struct PagedTcParams {
 // Units of up to 32 query rows; nr: 4, 8, 16 or 32 (>= the rows of a unit).
 cudaError_t launch_paged_decode(const PagedTcParams& p, int dtype, int pool_dtype, int nr,
                                 size_t smem, cudaStream_t stream);
+// Units in groups of 128 query rows.
+cudaError_t launch_paged_rows(const PagedTcParams& p, int dtype, int pool_dtype, size_t smem,
+                              cudaStream_t stream);
 // The partials of units cut between blocks.
 cudaError_t launch_paged_merge(const PagedTcParams& p, int dtype, cudaStream_t stream);
 

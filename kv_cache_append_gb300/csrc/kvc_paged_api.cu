@@ -84,21 +84,56 @@ int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 // then starts on an 8-row swizzle atom).
 struct TcPlan {
     bool ok = false;
-    int nr = 0;  // decode kernel: rows a unit is padded to
+    int nr = 0;  // decode kernel: rows a unit is padded to; 0: the rows kernel
     size_t smem = 0;
     int64_t bytes = 0, off_ml = 0, off_acc = 0;
     PagedTcParams p;
 };
 constexpr int64_t kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024, kSmemReserved = 1024;
 
+// records of the blocks, then their partials
+void tc_workspace(const kvc_paged_dims& d, TcPlan* t) {
+    const PagedTcParams& p = t->p;
+    t->off_ml = up(p.ctas * static_cast<int64_t>(sizeof(PagedRec)), 256);
+    t->off_acc = t->off_ml + up(int64_t(2) * p.ctas * p.RG * 8, 256);
+    t->bytes = t->off_acc + int64_t(2) * p.ctas * p.RG * d.Dv * 4;
+    t->ok = true;
+}
+
 TcPlan tc_plan(const kvc_paged_dims& d) {
     TcPlan t;
     const int64_t es = elem(d.pool_dtype), R = d.max_q * (d.Hq / d.Hk);
     if (d.dtype == KVC_F32 || d.D * es % 16 != 0 || d.Dv * es % 16 != 0 || d.Dv > 128 ||
-        d.block_size % 8 != 0 || R > 32 || d.total_q < 1)
+        d.block_size % 8 != 0 || d.total_q < 1)
         return t;
     std::memset(&t.p, 0, sizeof(t.p));
     PagedTcParams& p = t.p;
+    if (R > 32) {
+        // groups of 128 rows: query buffers, then rings of key and value tiles
+        const int64_t parts = es == 1 ? 2 : 1, nkb = (d.D * es + 127) / 128, nvb = (d.Dv * es + 127) / 128;
+        const int64_t kb = nkb * 128 * 128, vb = nvb * 128 * 128;
+        p.RG = 128;
+        p.hh = 128;
+        while (d.block_size % p.hh != 0) p.hh /= 2;
+        p.off_q = es == 1 ? 7168 : 3072;  // scales of 16 tiles, or none
+        p.q_bytes = static_cast<int>(parts * kb + (es == 1 ? 1024 : 0));
+        // the next run's query rows are prepared ahead where that leaves three tiles
+        int64_t room = kSmemBlock - p.off_q - 2 * p.q_bytes;
+        p.ni = room >= 3 * (kb + vb) ? 2 : 1;
+        room = kSmemBlock - p.off_q - p.ni * p.q_bytes;
+        const int64_t pairs = std::min<int64_t>(8, room / (kb + vb));
+        if (pairs < 1) return t;
+        room -= pairs * (kb + vb);
+        p.ns = static_cast<int>(pairs < 8 && room >= kb ? pairs + 1 : pairs);
+        if (p.ns > pairs) room -= kb;
+        p.nv = static_cast<int>(pairs < 8 && room >= vb ? pairs + 1 : pairs);
+        if (p.ns < 2) return t;
+        p.off_stage = p.off_q + p.ni * p.q_bytes;
+        t.smem = static_cast<size_t>(p.off_stage + p.ns * kb + p.nv * vb);
+        p.ctas = static_cast<int>(kPlanSms);
+        tc_workspace(d, &t);
+        return t;
+    }
     t.nr = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
     const int64_t dn = t.nr <= 16 ? 16 : 32, parts = es == 1 ? 2 : 1;
     const int64_t nkb = (d.D * es + 127) / 128, nvb = es == 1 ? 1 : 2, nblk = dn * 128;
@@ -109,25 +144,26 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
     p.q_bytes = static_cast<int>(up(parts * nkb * nblk + 32 * 12, 1024));
     const int64_t npt = es == 2 && dn == 16 ? 2 : 1;
     p.ni = 2;
-    p.off_item = 2048;
-    p.off_x = 2048 + 256;
-    p.off_q = static_cast<int>(up(p.off_x + 2 * t.nr * 16 + 32, 1024));
-    p.off_p = p.off_q + p.ni * p.q_bytes;
-    p.off_stage = static_cast<int>(p.off_p + npt * parts * (es == 1 ? 1 : 2) * nblk);
+    auto layout = [&](int64_t stages, int64_t cap) {  // scales, items, exchange, queries, weights, stages
+        p.off_item = static_cast<int>(1024 + stages * 256);
+        p.off_x = p.off_item + 256;
+        p.off_q = static_cast<int>(up(p.off_x + 2 * t.nr * 16 + 32, 1024));
+        p.off_p = p.off_q + p.ni * p.q_bytes;
+        p.off_stage = static_cast<int>(p.off_p + npt * parts * (es == 1 ? 1 : 2) * nblk);
+        p.ns = static_cast<int>(std::min(stages, (cap - p.off_stage) / p.stage_bytes));
+    };
     // two blocks an SM where each still has two stages or more (not for 32 rows,
     // whose registers take a whole SM)
     int64_t blocks = es == 1 && t.nr <= 16 ? 2 : 1;
-    int64_t room = kSmemSm / blocks - kSmemReserved - p.off_stage;
-    if (blocks == 2 && room < 2 * p.stage_bytes) blocks = 1;
-    if (blocks == 1) room = kSmemBlock - p.off_stage;
-    p.ns = static_cast<int>(std::min<int64_t>(8, room / p.stage_bytes));
+    if (blocks == 2) {
+        layout(4, kSmemSm / 2 - kSmemReserved);
+        if (p.ns < 2) blocks = 1;
+    }
+    if (blocks == 1) layout(8, kSmemBlock);
     if (p.ns < 2) return t;
     t.smem = static_cast<size_t>(p.off_stage + int64_t(p.ns) * p.stage_bytes);
     p.ctas = static_cast<int>(kPlanSms * blocks);
-    t.off_ml = up(p.ctas * static_cast<int64_t>(sizeof(PagedRec)), 256);
-    t.off_acc = t.off_ml + up(int64_t(2) * p.ctas * p.RG * 8, 256);
-    t.bytes = t.off_acc + int64_t(2) * p.ctas * p.RG * d.Dv * 4;
-    t.ok = true;
+    tc_workspace(d, &t);
     return t;
 }
 
@@ -265,7 +301,8 @@ int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int6
 
 const char* kvc_attend_paged_path(const kvc_paged_dims* dims) {
     if (kvc::check_paged(dims) != KVC_OK) return nullptr;
-    return kvc::tc_plan(*dims).ok ? "decode" : "cores";
+    const kvc::TcPlan t = kvc::tc_plan(*dims);
+    return !t.ok ? "cores" : t.nr ? "decode" : "rows";
 }
 
 size_t kvc_attend_paged_workspace_bytes(const kvc_paged_dims* dims) {
@@ -337,7 +374,7 @@ int kvc_attend_paged(const kvc_paged_dims* dims, const int64_t* q_strides, const
     // the tensor-core kernels read query rows in words of 8 bytes (split into
     // 8-bit parts) or 16 (copied)
     const int64_t qw = eight(d) ? 8 : 16;
-    if (t.ok && aligned(key_pool, 16) && aligned(value_pool, 16) && aligned(q, qw) &&
+    if (t.ok && (t.nr || aligned(out, 16)) && aligned(key_pool, 16) && aligned(value_pool, 16) && aligned(q, qw) &&
         q_strides[0] * es % qw == 0 && q_strides[1] * es % qw == 0 &&
         pool_map(&t.p.tk, key_pool, d, d.D, t.p.hh) && pool_map(&t.p.tv, value_pool, d, d.Dv, t.p.hh)) {
         unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -345,7 +382,8 @@ int kvc_attend_paged(const kvc_paged_dims* dims, const int64_t* q_strides, const
         t.p.rec = reinterpret_cast<PagedRec*>(ws);
         t.p.part_ml = reinterpret_cast<float*>(ws + t.off_ml);
         t.p.part_acc = reinterpret_cast<float*>(ws + t.off_acc);
-        cudaError_t e = launch_paged_decode(t.p, d.dtype, d.pool_dtype, t.nr, t.smem, stream);
+        cudaError_t e = t.nr ? launch_paged_decode(t.p, d.dtype, d.pool_dtype, t.nr, t.smem, stream)
+                             : launch_paged_rows(t.p, d.dtype, d.pool_dtype, t.smem, stream);
         if (e == cudaSuccess) e = launch_paged_merge(t.p, d.dtype, stream);
         return e == cudaSuccess ? KVC_OK : KVC_E_CUDA;
     }

@@ -72,7 +72,7 @@ struct Bars {
     __device__ uint32_t drained() const { return base + 264u; }
 };
 constexpr int kTmemSlot = 272, kAbort = 276, kBad = 280 /* [4] */, kOdd = 296 /* [2] */;
-// PagedStart at 512 (32 sums and 4 words), StageScales from 1024
+// PagedStart at 512 (32 sums and 4 words), the stages' StageScales from 1024
 
 // What a run's query buffer holds behind the rows: per row the factor of its
 // products, its position (-1: no row) and its bias slope (times log2 e).
@@ -176,48 +176,17 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
                 if (lane == 0) rd->mul[r] = a.scale;
             } else {
                 float x[2][4];
-                float big = 0.f;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int d = c * 128 + lane * 4;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
-                    if (live && d < a.D) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(q + d);
-                        const T* h = reinterpret_cast<const T*>(&v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[c][e] = Storage<T>::to_float(h[e]);
-                            if (fabsf(x[c][e]) < INFINITY)
-                                big = fmaxf(big, fabsf(x[c][e]));
-                            else
-                                x[c][e] = __uint_as_float(0x7fffffffu);  // no 8-bit infinity: NaN
-                        }
-                    }
-                }
-                big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-                // 2^e: the row's largest element then lies in [2^7, 2^8)
-                int e2 = 7 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
-                e2 = max(-120, min(120, e2));
-                const float f = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+                const float f = load_row_part<T>(q, a.D, live, lane, x);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if (c >= nkb) break;
-                    uint32_t hi = 0, lo = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float u = x[c][e] * f, v = x[c][e + 1] * f;
-                        const uint32_t h2 = to_eight2<false>(u, v);
-                        const float2 hf = from_eight2<false>(h2);
-                        hi |= h2 << (8 * e);
-                        lo |= to_eight2<false>(u - hf.x, v - hf.y) << (8 * e);
-                    }
+                    uint32_t hi, lo;
+                    split_row_part(x[c], f, hi, lo);
                     const int o = c * S::nblk + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
                     *reinterpret_cast<uint32_t*>(sq + o) = hi;
                     *reinterpret_cast<uint32_t*>(sq + nkb * S::nblk + o) = lo;
                 }
-                if (lane == 0)
-                    rd->mul[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+                if (lane == 0) rd->mul[r] = a.scale * (1.f / f);  // f is a power of two
             }
         }
         fence_async_shared();  // the query rows, for the tensor cores
@@ -252,9 +221,10 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
             }
             const uint32_t sK = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes;
             const uint32_t sV = sK + static_cast<uint32_t>(nkb * kTS * 128);
-            if (!paged_load_tile<EB, kTS>(p, it, it.tile0 + n, sK, sV, nkb, nvb, sc + ring.s,
-                                          bars.full(ring.s)) &&
-                lane == 0) {
+            const PagedBoxes x = paged_boxes<EB, kTS>(p, it, it.tile0 + n, sc + ring.s);
+            paged_load_boxes<EB, kTS>(p, &p.tk, x, sK, nkb, bars.full(ring.s), true, nvb);
+            paged_load_boxes<EB, kTS>(p, &p.tv, x, sV, nvb, bars.full(ring.s), false);
+            if (x.bad && lane == 0) {
                 *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 1;
                 if (a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
             }
@@ -377,23 +347,6 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
     mbar_wait(bars.drained(), 0u, &never);
 }
 
-// 32-bit words whose 8- or 16-bit fields that hold an infinity or NaN are cleared.
-template <int EB, typename T>
-__device__ __forceinline__ uint32_t clear_odd(uint32_t w, bool e5m2) {
-    uint32_t keep = 0xffffffffu;
-    if (EB == 2) {
-        const uint32_t inf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
-        if ((w & 0x7fffu) >= inf) keep &= 0xffff0000u;
-        if (((w >> 16) & 0x7fffu) >= inf) keep &= 0x0000ffffu;
-    } else {
-        const uint32_t inf = e5m2 ? 0x7cu : 0x7fu;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (((w >> (8 * i)) & 0x7fu) >= inf) keep &= ~(0xffu << (8 * i));
-    }
-    return w & keep;
-}
-
 template <typename T, int EB, int NR, bool MOD>
 __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars bars,
                               volatile int* abort, uint32_t tmem, const PagedStart* st) {
@@ -465,10 +418,10 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             if (lane == 0) mbar_arrive(bars.s_free(sb), 1u);
             float ksc = 1.f, ivs = 1.f, lv = 0.f;  // key scale, 1 / value scale, its log2
             if (EB == 1) {
-                const float2 kv = scales[ring.s].kv[t >> box];
+                const float4 kv = scales[ring.s].kv[t >> box];
                 ksc = kv.x;
-                ivs = 1.f / kv.y;
-                lv = __log2f(kv.y);
+                lv = kv.z;
+                ivs = kv.w;
             }
             const int j0 = (it.tile0 + n) * kTS, j = j0 + t;
             // a tile with a slot that some row does not see
@@ -548,9 +501,8 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             if (EB == 1) {
 #pragma unroll
                 for (int r = 0; r < NR; r += 2) {
-                    const uint32_t hi = to_eight2<false>(sv[r], sv[r + 1]);
-                    const float2 hf = from_eight2<false>(hi);
-                    const uint32_t lo = to_eight2<true>(sv[r] - hf.x, sv[r + 1] - hf.y);
+                    uint32_t hi, lo;
+                    split_weights(sv[r], sv[r + 1], hi, lo);
                     unsigned char* o0 = pb + r * 128 + (((t >> 4) ^ (r & 7)) << 4) + (t & 15);
                     unsigned char* o1 = pb + (r + 1) * 128 + (((t >> 4) ^ ((r + 1) & 7)) << 4) + (t & 15);
                     o0[0] = static_cast<unsigned char>(hi);

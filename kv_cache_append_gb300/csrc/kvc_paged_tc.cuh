@@ -16,6 +16,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kvc_launch.h"
 #include "kvc_paged.cuh"
 #include "kvc_pipeline.cuh"
@@ -252,29 +254,34 @@ __device__ __forceinline__ void paged_record(const PagedTcParams& p, const Paged
     p.rec[blockIdx.x] = r;
 }
 
-// Per stage: the key and value scale of each box of the tile.
+// Of each box of a tile: key scale, value scale, its log2 and its inverse.
 constexpr int kMaxBoxes = 16;
 struct StageScales {
-    float2 kv[kMaxBoxes];
+    float4 kv[kMaxBoxes];
 };
 
-// One tile's boxes (rows of one pool block each), by a whole warp: those
-// holding a visible slot. Returns false when a block id lies outside the pool
-// (block 0 is read instead).
+// One tile's boxes (rows of one pool block each) that hold a visible slot: a
+// lane each. `bad`: a block id lies outside the pool (block 0 is read instead).
+struct PagedBoxes {
+    int pa, pb;  // boxes [pa, pb)
+    int y, z;    // this lane's box: its first row in the block, its pool unit
+    bool bad;
+};
 template <int EB, int TS>
-__device__ __forceinline__ bool paged_load_tile(const PagedTcParams& p, const PagedItem& it, int tile,
-                                                uint32_t sK, uint32_t sV, int nkb, int nvb,
-                                                StageScales* sc, uint32_t full) {
-    constexpr int kElems = 128 / EB;  // elements of a 128-byte column block
+__device__ __forceinline__ PagedBoxes paged_boxes(const PagedTcParams& p, const PagedItem& it,
+                                                  int tile, StageScales* sc) {
     const PagedAttendParams& a = p.a;
     const int lane = threadIdx.x & 31;
     const int j0 = tile * TS, hh = p.hh;
-    const int pa = max(0, it.lo - j0) / hh, pb = (min(TS, it.last + 1 - j0) + hh - 1) / hh;
-    int id = 0, y = 0;
+    PagedBoxes x;
+    x.pa = max(0, it.lo - j0) / hh;
+    x.pb = (min(TS, it.last + 1 - j0) + hh - 1) / hh;
+    int id = 0;
+    x.y = 0;
     bool bad = false;
-    if (lane >= pa && lane < pb) {
+    if (lane >= x.pa && lane < x.pb) {
         const int slot = j0 + lane * hh, blk = slot / a.bs;
-        y = slot - blk * a.bs;
+        x.y = slot - blk * a.bs;
         id = a.table[it.b * a.max_blocks + blk];
         if (id < 0 || id >= a.num_blocks) {
             bad = true;
@@ -282,26 +289,99 @@ __device__ __forceinline__ bool paged_load_tile(const PagedTcParams& p, const Pa
         }
         if (EB == 1) {
             const int64_t u = static_cast<int64_t>(id) * a.Hk + it.hk;
-            sc->kv[lane] = make_float2(a.ks[u], a.vs[u]);
+            const float vs = a.vs[u];
+            sc->kv[lane] = make_float4(a.ks[u], vs, __log2f(vs), __fdiv_rn(1.f, vs));
         }
     }
-    __syncwarp();  // the scales are written before lane 0's arrive publishes the stage
-    const int nb = nkb + nvb, n = (pb - pa) * nb;
-    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * hh * 128));
+    x.z = id * a.Hk + it.hk;
+    x.bad = __any_sync(0xffffffffu, bad);
+    return x;
+}
+// Their copies, `nb` column blocks of 128 bytes each, spread over the warp.
+template <int EB, int TS>
+__device__ __forceinline__ void paged_load_boxes(const PagedTcParams& p, const CUtensorMap* map,
+                                                 const PagedBoxes& x, uint32_t dst, int nb,
+                                                 uint32_t full, bool expect = true, int extra = 0) {
+    constexpr int kElems = 128 / EB;  // elements of a column block
+    const int lane = threadIdx.x & 31, hh = p.hh, n = (x.pb - x.pa) * nb;
+    __syncwarp();  // the scales are written before lane 0's arrive publishes the tile
+    if (expect && lane == 0)
+        mbar_arrive_expect_tx(full, static_cast<uint32_t>((x.pb - x.pa) * (nb + extra) * hh * 128));
     __syncwarp();
-    const int z0 = id * a.Hk + it.hk;
     for (int base = 0; base < n; base += 32) {
-        const int l = base + lane, c = pa + l / nb, k = l % nb;
-        const int z = __shfl_sync(0xffffffffu, z0, c & 31), yy = __shfl_sync(0xffffffffu, y, c & 31);
-        if (l < n) {
-            const uint32_t o = static_cast<uint32_t>(c * hh * 128);
-            if (k < nkb)
-                tma_load_3d(sK + k * TS * 128 + o, &p.tk, kElems * k, yy, z, full);
-            else
-                tma_load_3d(sV + (k - nkb) * TS * 128 + o, &p.tv, kElems * (k - nkb), yy, z, full);
+        const int l = base + lane, c = x.pa + l / nb, k = l % nb;
+        const int z = __shfl_sync(0xffffffffu, x.z, c & 31), y = __shfl_sync(0xffffffffu, x.y, c & 31);
+        if (l < n)
+            tma_load_3d(dst + k * TS * 128 + static_cast<uint32_t>(c * hh * 128), map, kElems * k, y, z,
+                        full);
+    }
+}
+
+// A query row for the 8-bit products, a warp at a time (lane: elements 4 lane ..
+// of each 128): its elements, and the power of two that takes the largest into
+// [2^7, 2^8).
+template <typename T>
+__device__ __forceinline__ float load_row_part(const T* q, int D, bool live, int lane, float (&x)[2][4]) {
+    float big = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int d = c * 128 + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
+        if (live && d < D) {
+            const uint2 v = *reinterpret_cast<const uint2*>(q + d);
+            const T* h = reinterpret_cast<const T*>(&v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[c][e] = Storage<T>::to_float(h[e]);
+                if (fabsf(x[c][e]) < INFINITY)
+                    big = fmaxf(big, fabsf(x[c][e]));
+                else
+                    x[c][e] = __uint_as_float(0x7fffffffu);  // no 8-bit infinity: NaN
+            }
         }
     }
-    return !__any_sync(0xffffffffu, bad);
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    int e2 = 7 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
+    e2 = max(-120, min(120, e2));
+    return __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+}
+// Four of its elements, scaled, as hi + lo, both e4m3.
+__device__ __forceinline__ void split_row_part(const float (&x)[4], float f, uint32_t& hi, uint32_t& lo) {
+    hi = lo = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const float u = x[e] * f, v = x[e + 1] * f;
+        const uint32_t h2 = to_eight2<false>(u, v);
+        const float2 hf = from_eight2<false>(h2);
+        hi |= h2 << (8 * e);
+        lo |= to_eight2<false>(u - hf.x, v - hf.y) << (8 * e);
+    }
+}
+// Two weights (up to 448) as hi (e4m3) + lo (e5m2), by way of fp16, in which
+// the difference is exact.
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 w = __floats2half2_rn(a, b);
+    hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(w), __NV_SATFINITE, __NV_E4M3);
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(w, h)), __NV_SATFINITE, __NV_E5M2);
+}
+
+// A word of 8- or 16-bit elements with those that are an infinity or NaN cleared.
+template <int EB, typename T>
+__device__ __forceinline__ uint32_t clear_odd(uint32_t w, bool e5m2) {
+    uint32_t keep = 0xffffffffu;
+    if (EB == 2) {
+        const uint32_t inf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+        if ((w & 0x7fffu) >= inf) keep &= 0xffff0000u;
+        if (((w >> 16) & 0x7fffu) >= inf) keep &= 0x0000ffffu;
+    } else {
+        const uint32_t inf = e5m2 ? 0x7cu : 0x7fu;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (((w >> (8 * i)) & 0x7fu) >= inf) keep &= ~(0xffu << (8 * i));
+    }
+    return w & keep;
 }
 
 }  // namespace kvc
