@@ -436,7 +436,6 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                     if (j <= lim && (a.window == 0 || j > lim - a.window)) seen |= 1u << r;
                 }
             }
-            if (seen == 0u) ivs = 0.f;  // its box may not have been read
             bool need = false;
 #pragma unroll
             for (int r = 0; r < NR; r += 4) {
@@ -667,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
         tmem_relinquish();
     }
     tc_fence_before();
-    paged_plan<kTS, kThreads>(p, st);  // with block barriers
+    paged_plan<T, kTS, kThreads>(p, st);  // with block barriers
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemSlot);
     launch_dependents();
@@ -690,7 +689,6 @@ __global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
         tmem_dealloc(tmem, S::cols);
     }
     if (threadIdx.x == 0 && *abort && p.a.status) atomicOr(p.a.status, KVC_DEV_TIMEOUT);
-    paged_zero_invalid<T, kThreads>(p);
 }
 
 // Block (c, y): the unit whose second block is c, rows y, y + gridDim.y, ...

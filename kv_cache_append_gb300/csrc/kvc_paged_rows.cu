@@ -354,44 +354,60 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             const int j0 = (it.tile0 + n) * kTS;
             const bool edge = j0 + kTS - 1 > it.first || (a.window > 0 && j0 <= it.last - a.window);
             const StageScales* sc = scales + c % kScaleRing;
-            // first pass: the row's largest score of the tile (with a cap or
-            // bias, the scores go back to tensor memory)
-            float top = -INFINITY;
+            float s[kTS];  // the row's scores of the tile, then its weights
+            tmem_ld128(tS, s);
+            if (MOD) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float s[32];
-                tmem_ld32(tS + 32 * q, s);
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < kTS; e += 8) {
                     float f = mul, lv = 0.f;
                     if (EB == 1) {
-                        const float4 kv = sc->kv[(32 * q + e) >> box];
+                        const float4 kv = sc->kv[e >> box];
                         f *= kv.x;
                         lv = kv.z;
                     }
+                    if (a.softcap > 0.f) {
+                        // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+                        f *= cap_in;
 #pragma unroll
-                    for (int i = e; i < e + 8; ++i) {
-                        const int j = j0 + 32 * q + i;
-                        float v;
-                        if (MOD) {
-                            v = s[i] * f;
-                            if (a.softcap > 0.f) {
-                                const float ex = fast_exp2(v * cap_in);
-                                v = cap_out - __fdividef(2.f * cap_out, 1.f + ex);
-                                if (!(ex < INFINITY)) v = ex == ex ? cap_out : ex;
-                            } else {
-                                v *= kLog2e;
-                            }
-                            v = v - slope * static_cast<float>(lim - j) + lv;
-                        } else {
-                            v = fmaf(s[i], f, lv);
-                        }
-                        if (edge && (j > lim || j <= low)) v = -INFINITY;
-                        top = fmaxf(top, v);
-                        if (MOD) s[i] = v;
+                        for (int i = e; i < e + 8; ++i)
+                            s[i] = fmaf(-2.f * cap_out, fast_rcp(1.f + fast_exp2(s[i] * f)),
+                                        cap_out + lv);
+                    } else {
+                        f *= kLog2e;
+#pragma unroll
+                        for (int i = e; i < e + 8; ++i) s[i] = fmaf(s[i], f, lv);
+                    }
+                    if (a.slopes) {
+                        const float far = slope * static_cast<float>(lim - j0 - e);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            s[e + i] += fmaf(slope, static_cast<float>(i), -far);
                     }
                 }
-                if (MOD) tmem_st32(tS + 32 * q, s);
+            }
+            if (edge) {
+                const int hi = lim - j0, lo = low - j0;
+#pragma unroll
+                for (int i = 0; i < kTS; ++i)
+                    if (i > hi || i <= lo) s[i] = -INFINITY;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kTS; e += 8) {
+                float m = fmaxf(fmaxf(s[e], s[e + 1]), s[e + 2]);
+                m = fmaxf(fmaxf(m, s[e + 3]), s[e + 4]);
+                m = fmaxf(fmaxf(m, s[e + 5]), s[e + 6]);
+                m = fmaxf(m, s[e + 7]);
+                if (!MOD) {
+                    float f = mul, lv = 0.f;
+                    if (EB == 1) {
+                        const float4 kv = sc->kv[e >> box];
+                        f = fmaxf(f * kv.x, 1e-37f);
+                        lv = kv.z;
+                    }
+                    m = fmaf(m, f, lv);
+                }
+                top = fmaxf(top, m);
             }
             float corr = 1.f;
             if (top > ref + Threshold<EB>::v) {
@@ -401,9 +417,9 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             }
             if (__any_sync(0xffffffffu, corr != 1.f) && any) {
                 // O is at rest: S of this tile was issued after the group's last product
-                // (a row without a sum yet holds zeros, or what 0 makes of them)
                 if (!warp_wait(bars.o_done(g), static_cast<uint32_t>((c / 2 - 1) & 1), abort)) return;
                 tc_fence_after();
+#pragma unroll 1
                 for (int d = 0; d < a.Dv; d += 16) {
                     float o[16];
                     tmem_ldn<16>(tO + 128 * g + d, o);
@@ -413,47 +429,46 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 }
             }
             any = true;
-            // second pass: the weights, over the scores
-            const float off = kOffset - ref;
+            // the weights, over the scores (a row that saw nothing yet: all 2^-inf)
+            const float off = ref == -INFINITY ? kOffset : kOffset - ref;
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float s[32];
-                tmem_ld32(tS + 32 * q, s);
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
-                    float f = mul, lv = off, ivs = 1.f;
+                    float f = MOD ? 1.f : mul, lv = off, ivs = 1.f;
                     if (EB == 1) {
                         const float4 kv = sc->kv[(32 * q + e) >> box];
-                        f *= kv.x;
-                        lv += kv.z;
-                        ivs = kv.w;
-                    }
-#pragma unroll
-                    for (int i = e; i < e + 8; ++i) {
-                        const int j = j0 + 32 * q + i;
-                        float v = fast_exp2(MOD ? s[i] + off : fmaf(s[i], f, lv));
-                        const bool hide = edge && (j > lim || j <= low);
-                        if (hide) v = 0.f;
-                        s[i] = v;
-                        if (EB == 1) {
-                            if (!hide) l = fmaf(v, ivs, l);
-                        } else {
-                            l += v;
+                        if (!MOD) {
+                            f = fmaxf(f * kv.x, 1e-37f);
+                            lv += kv.z;
                         }
+                        ivs = kv.w;
+                        sum = make_float2(0.f, 0.f);
+                    }
+                    float* x = s + 32 * q + e;
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 v = fma2(make_float2(x[i], x[i + 1]), make_float2(f, f),
+                                              make_float2(lv, lv));
+                        x[i] = fast_exp2(v.x);
+                        x[i + 1] = fast_exp2(v.y);
+                        sum = add2(sum, make_float2(x[i], x[i + 1]));
                     }
                     if (EB == 1) {
+                        l = fmaf(sum.x + sum.y, ivs, l);
 #pragma unroll
-                        for (int i = e; i < e + 8; i += 4) {
+                        for (int i = 0; i < 8; i += 4) {
                             uint32_t h0, l0, h1, l1;
-                            split_weights(s[i], s[i + 1], h0, l0);
-                            split_weights(s[i + 2], s[i + 3], h1, l1);
-                            w[i / 4] = h0 | (h1 << 16);
-                            w[8 + i / 4] = l0 | (l1 << 16);
+                            split_weights(x[i], x[i + 1], h0, l0);
+                            split_weights(x[i + 2], x[i + 3], h1, l1);
+                            w[(e + i) / 4] = h0 | (h1 << 16);
+                            w[8 + (e + i) / 4] = l0 | (l1 << 16);
                         }
                     } else {
 #pragma unroll
-                        for (int i = e; i < e + 8; i += 2) w[i / 2] = pack2<T>(s[i], s[i + 1]);
+                        for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack2<T>(x[i], x[i + 1]);
                     }
                 }
                 float wf[16];
@@ -461,6 +476,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 for (int i = 0; i < 16; ++i) wf[i] = __uint_as_float(w[i]);
                 tmem_stn<16>(tS + 16 * q, wf);
             }
+            if (EB == 2) l += sum.x + sum.y;
             if (edge) {  // thread r looks after slot r's value row
                 if (!warp_wait(bars.v_full(stage), sph, abort)) return;
                 const int j = j0 + r;
@@ -616,21 +632,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         tmem_relinquish();
     }
     tc_fence_before();
-    paged_plan<kTS, kThreads>(p, st);  // with block barriers
+    paged_plan<T, kTS, kThreads>(p, st);  // with block barriers
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemSlot);
     launch_dependents();
 
+    // the softmax threads keep a tile's row in registers: 192 each, 64 for the others
+    // (8 warps x 192 + 8 x 64 = the launch's 16 x 128)
     if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         softmax_warps<T, EB, MOD>(p, smem, bars, abort, tmem);
-    } else if (warp == kSWarp) {
-        if ((threadIdx.x & 31) == 0) s_issuer<T, EB>(p, smem, bars, abort, tmem);
-    } else if (warp == kPvWarp) {
-        if ((threadIdx.x & 31) == 0) pv_issuer<T, EB>(p, smem, bars, abort, tmem);
-    } else if (warp == kProdWarp) {
-        producer_warp<EB>(p, smem, bars, abort);
-    } else if (warp >= kQWarp) {
-        query_warps<T, EB>(p, smem, bars, st, abort);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kSWarp) {
+            if ((threadIdx.x & 31) == 0) s_issuer<T, EB>(p, smem, bars, abort, tmem);
+        } else if (warp == kPvWarp) {
+            if ((threadIdx.x & 31) == 0) pv_issuer<T, EB>(p, smem, bars, abort, tmem);
+        } else if (warp == kProdWarp) {
+            producer_warp<EB>(p, smem, bars, abort);
+        } else if (warp >= kQWarp) {
+            query_warps<T, EB>(p, smem, bars, st, abort);
+        }
     }
     tc_fence_before();
     __syncthreads();  // every thread reaches this exactly once: all waits are bounded
@@ -639,7 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         tmem_dealloc(tmem, 512);
     }
     if (threadIdx.x == 0 && *abort && p.a.status) atomicOr(p.a.status, KVC_DEV_TIMEOUT);
-    paged_zero_invalid<T, kThreads>(p);
 }
 
 template <typename T, int EB, bool MOD>

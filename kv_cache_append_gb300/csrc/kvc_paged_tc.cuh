@@ -88,9 +88,10 @@ struct PagedStart {
 };
 
 template <int TS>
-__device__ __forceinline__ long long paged_seq_tiles(const PagedTcParams& p, int64_t b) {
+__device__ __forceinline__ long long paged_seq_tiles(const PagedTcParams& p, int64_t b, int* invalid) {
     const PagedAttendParams& a = p.a;
     const PagedSeq s = paged_seq(a.cu, a.kl, b, a.total_q, a.max_q, a.M);
+    if (!s.ok) *invalid = 1;
     if (!s.ok || s.S == 0) return 0;
     long long n = 0;
     const int ng = paged_groups(a, p.RG, s.S);
@@ -98,15 +99,18 @@ __device__ __forceinline__ long long paged_seq_tiles(const PagedTcParams& p, int
     return n * a.Hk;
 }
 
-// All threads; ends with a block barrier.
-template <int TS, int THREADS>
+// All threads; ends with a block barrier. Where a sequence lies outside the
+// contract, block c also writes the zero rows of sequences c, c + grid, ...
+template <typename T, int TS, int THREADS>
 __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* st) {
-    const int64_t B = p.a.B;
+    const PagedAttendParams& a = p.a;
+    const int64_t B = a.B;
     const int64_t per_thread = (B + THREADS - 1) / THREADS;
     const int64_t b0 = min(B, threadIdx.x * per_thread), b1 = min(B, b0 + per_thread);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long mine = 0;
-    for (int64_t b = b0; b < b1; ++b) mine += paged_seq_tiles<TS>(p, b);
+    int invalid = 0;
+    for (int64_t b = b0; b < b1; ++b) mine += paged_seq_tiles<TS>(p, b, &invalid);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -114,7 +118,7 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
         if (lane >= o) incl += v;
     }
     if (lane == 31) st->sums[warp] = incl;
-    __syncthreads();
+    invalid = __syncthreads_or(invalid);
     long long before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
@@ -131,7 +135,7 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
     }
     if (at >= cur && at < cur + mine) {
         for (int64_t b = b0; b < b1; ++b) {
-            const long long n = paged_seq_tiles<TS>(p, b);
+            const long long n = paged_seq_tiles<TS>(p, b, &invalid);
             if (at < cur + n) {
                 st->b = static_cast<int>(b);
                 st->off = at - cur;
@@ -140,22 +144,17 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
             cur += n;
         }
     }
-    __syncthreads();
-}
-
-// Rows of sequences outside the contract are zero; their count is not large,
-// so block c sees to sequences c, c + grid, ...
-template <typename T, int THREADS>
-__device__ __forceinline__ void paged_zero_invalid(const PagedTcParams& p) {
-    const PagedAttendParams& a = p.a;
-    for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const PagedSeq s = paged_seq(a.cu, a.kl, b, a.total_q, a.max_q, a.M);
-        if (s.ok) continue;
-        if (threadIdx.x == 0 && a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
-        const int64_t n = static_cast<int64_t>(s.S) * a.Hq * a.Dv;
-        T* o = static_cast<T*>(a.out) + static_cast<int64_t>(s.q0) * a.Hq * a.Dv;
-        for (int64_t i = threadIdx.x; i < n; i += THREADS) o[i] = Storage<T>::from_float(0.f);
+    if (invalid) {
+        for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
+            const PagedSeq s = paged_seq(a.cu, a.kl, b, a.total_q, a.max_q, a.M);
+            if (s.ok) continue;
+            if (threadIdx.x == 0 && a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
+            const int64_t n = static_cast<int64_t>(s.S) * a.Hq * a.Dv;
+            T* o = static_cast<T*>(a.out) + static_cast<int64_t>(s.q0) * a.Hq * a.Dv;
+            for (int64_t i = threadIdx.x; i < n; i += THREADS) o[i] = Storage<T>::from_float(0.f);
+        }
     }
+    __syncthreads();
 }
 
 // The scheduling warp's walk over its block's runs (all lanes alike).
@@ -279,6 +278,8 @@ __device__ __forceinline__ PagedBoxes paged_boxes(const PagedTcParams& p, const 
     int id = 0;
     x.y = 0;
     bool bad = false;
+    if (EB == 1 && lane < kMaxBoxes && (lane < x.pa || lane >= x.pb))
+        sc->kv[lane] = make_float4(1.f, 1.f, 0.f, 1.f);  // masked slots: anything finite
     if (lane >= x.pa && lane < x.pb) {
         const int slot = j0 + lane * hh, blk = slot / a.bs;
         x.y = slot - blk * a.bs;
