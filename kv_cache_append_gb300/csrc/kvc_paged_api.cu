@@ -141,22 +141,22 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
     p.hh = 128;
     while (d.block_size % p.hh != 0) p.hh /= 2;
     p.stage_bytes = static_cast<int>((nkb + nvb) * 128 * 128);
-    p.q_bytes = static_cast<int>(up(parts * nkb * nblk + 32 * 12, 1024));
+    p.q_bytes = static_cast<int>(parts * nkb * nblk);
     const int64_t npt = es == 2 && dn == 16 ? 2 : 1;
     p.ni = 2;
     auto layout = [&](int64_t stages, int64_t cap) {  // scales, items, exchange, queries, weights, stages
-        p.off_item = static_cast<int>(1024 + stages * 256);
-        p.off_x = p.off_item + 256;
+        p.off_item = static_cast<int>(512 + std::max<int64_t>(320, stages * 256));
+        p.off_x = p.off_item + 128 + 2 * 384;
         p.off_q = static_cast<int>(up(p.off_x + 2 * t.nr * 16 + 32, 1024));
         p.off_p = p.off_q + p.ni * p.q_bytes;
-        p.off_stage = static_cast<int>(p.off_p + npt * parts * (es == 1 ? 1 : 2) * nblk);
+        p.off_stage = static_cast<int>(p.off_p + npt * (es == 1 ? 3 : 2) * nblk);
         p.ns = static_cast<int>(std::min(stages, (cap - p.off_stage) / p.stage_bytes));
     };
     // two blocks an SM where each still has two stages or more (not for 32 rows,
     // whose registers take a whole SM)
     int64_t blocks = es == 1 && t.nr <= 16 ? 2 : 1;
     if (blocks == 2) {
-        layout(4, kSmemSm / 2 - kSmemReserved);
+        layout(3, kSmemSm / 2 - kSmemReserved);
         if (p.ns < 2) blocks = 1;
     }
     if (blocks == 1) layout(8, kSmemBlock);

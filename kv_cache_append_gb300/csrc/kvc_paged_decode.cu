@@ -15,16 +15,15 @@
 // products of both parts add up in the same accumulator.
 //   Query rows: x 2^k = hi + lo, both e4m3, k from the row's largest element
 //   (2^7..2^8 then). 4 + 4 significant bits: bf16 exactly, fp16 to 2^-8 of an element.
-//   Weights: w = hi (e4m3) + lo (e5m2). lo takes what hi leaves, down to 2^-17
-//   where e4m3 ends at 2^-10; with w up to 2^8.75 a weight is exact to 2^-7
-//   over 2^18 below the largest and not lost before 2^25 below it. (Two e4m3 parts
-//   would drop weights 2^-18 below the largest: the flat rest behind one dominant
-//   slot of a long context.)
+//   Weights: three e5m2 parts of an fp16 value (split_weights): 2^-9 of the weight
+//   over 16 octaves below the largest, 2^-25 of the largest under that. (e4m3 parts
+//   end at 2^-10: they would drop the flat rest behind one dominant slot of
+//   a long context.)
 // The key scale of a slot's block multiplies its scores. The value scale goes into
 // the weight: w = 2^(s + log2 vs - ref), and the row sum takes w / vs, so one
 // reference per row bounds the weights whatever the blocks' scales are.
-// N is padded to 16 anyway, so the second part costs nothing that matters: the
-// tensor cores are idle most of the time.
+// The further parts cost nothing that matters: the tensor cores are idle most of
+// the time.
 //
 // Warps: 4 softmax warps (a thread owns a slot), one S issuer, one P.V issuer,
 // one producer (block-table look-ups, scales, TMA boxes), one scheduler, which walks
@@ -49,15 +48,6 @@ namespace {
 constexpr int kTS = 128;
 constexpr int kMmaWarp = 4, kPvWarp = 5, kProdWarp = 6;  // warp 7 schedules
 constexpr int kThreads = 8 * 32;
-constexpr float kOffset = 7.f;  // weights are 2^(s - ref + 7)
-
-template <int EB>
-struct Threshold {
-    // a row's reference is raised when a score exceeds it by more: 8-bit weights
-    // end at 448 = 2^8.8, 16-bit ones at 2^15 and more
-    static constexpr float v = EB == 1 ? 1.75f : 8.f;
-};
-
 struct Bars {
     uint32_t base;
     __device__ uint32_t full(int s) const { return base + 8u * s; }
@@ -72,9 +62,10 @@ struct Bars {
     __device__ uint32_t drained() const { return base + 264u; }
 };
 constexpr int kTmemSlot = 272, kAbort = 276, kBad = 280 /* [4] */, kOdd = 296 /* [2] */;
-// PagedStart at 512 (32 sums and 4 words), the stages' StageScales from 1024
+// from 512: PagedStart (read before the first tile is loaded), then the stages'
+// StageScales; then the items and their rows' data
 
-// What a run's query buffer holds behind the rows: per row the factor of its
+// What a run holds besides the query rows: per row the factor of its
 // products, its position (-1: no row) and its bias slope (times log2 e).
 struct RowData {
     float mul[32];
@@ -84,10 +75,11 @@ struct RowData {
 
 template <int EB, int DN>
 struct Shape {
-    static constexpr int kParts = EB == 1 ? 2 : 1;         // of a query row, and of a weight
+    static constexpr int kParts = EB == 1 ? 2 : 1;         // of a query row
+    static constexpr int kWParts = EB == 1 ? 3 : 1;        // of a weight
     static constexpr int nblk = DN * 128;                  // a 128-byte column block of Q or P^T
     static constexpr int pblks = EB == 1 ? 1 : 2;          // column blocks of 128 weights
-    static constexpr int pbytes = kParts * pblks * nblk;   // one P^T buffer
+    static constexpr int pbytes = kWParts * pblks * nblk;  // one P^T buffer
     static constexpr int npt = (EB == 2 && DN == 16) ? 2 : 1;  // P^T buffers
     static constexpr uint32_t col_o = 2 * DN;
     static constexpr uint32_t cols = DN == 16 ? 64 : 128;
@@ -148,7 +140,7 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
             return;
         }
         unsigned char* sq = smem + p.off_q + kb * p.q_bytes;
-        RowData* rd = reinterpret_cast<RowData*>(sq + S::kParts * nkb * S::nblk);
+        RowData* rd = reinterpret_cast<RowData*>(smem + p.off_item + 128) + kb;
         const int R = it.S * a.G;
         if (lane == 0) {
             items[kb] = it;
@@ -202,7 +194,7 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
     const PagedAttendParams& a = p.a;
     const int lane = threadIdx.x & 31;
     const uint32_t stage0 = smem_addr(smem + p.off_stage);
-    StageScales* sc = reinterpret_cast<StageScales*>(smem + 1024);
+    StageScales* sc = reinterpret_cast<StageScales*>(smem + 512);
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
     const int nkb = (a.D * EB + 127) / 128;
     const int nvb = EB == 1 ? 1 : 2;  // value columns padded to 128: the boxes past them read zeros
@@ -322,12 +314,12 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
             const uint32_t sP = smem_addr(smem + p.off_p) + pb * S::pbytes;
             if (EB == 1) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)  // e4m3, then what it leaves in e5m2
+                for (int part = 0; part < 3; ++part)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)       // 32 slots per instruction
                         tc_mma_f8(tmem + S::col_o, smem_desc_sw128(sV + i * 32 * 128, 16, 1024),
                                   smem_desc_sw128(sP + part * S::nblk + i * 32, 16, 1024),
-                                  mma_idesc_f8(128, DN, a.e5m2, part != 0, true, false),
+                                  mma_idesc_f8(128, DN, a.e5m2, true, true, false),
                                   n != 0 || (part | i) != 0);
             } else {
 #pragma unroll
@@ -358,7 +350,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
-    const StageScales* scales = reinterpret_cast<const StageScales*>(smem + 1024);
+    const StageScales* scales = reinterpret_cast<const StageScales*>(smem + 512);
     // exchange: values [2][NR][4], flags [2][4]
     float* xval = reinterpret_cast<float*>(smem + p.off_x);
     int* xflag = reinterpret_cast<int*>(smem + p.off_x + 2 * NR * 4 * 4);
@@ -392,8 +384,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) return;
         const PagedItem it = items[kb];
         if (it.flags & kItemDone) return;
-        const RowData* rd = reinterpret_cast<const RowData*>(smem + p.off_q + kb * p.q_bytes +
-                                                             S::kParts * nkb * S::nblk);
+        const RowData* rd = reinterpret_cast<const RowData*>(smem + p.off_item + 128) + kb;
         // set behind this run's first meeting, read behind its last
         volatile int* odd = reinterpret_cast<volatile int*>(smem + kOdd + 4 * (k & 1));
         if (threadIdx.x == 0) *odd = 0;
@@ -458,7 +449,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                     s += lv;
                     if (!((seen >> (r + e)) & 1u)) s = -INFINITY;
                     sv[r + e] = s;
-                    need |= s > mref[r + e] + Threshold<EB>::v;
+                    need |= s > mref[r + e] + RaiseAbove<EB>::v;
                 }
             }
             // the references are raised for the whole tile or not at all
@@ -479,7 +470,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                     const float4 q4 = *reinterpret_cast<const float4*>(xval + (bm * NR + r) * 4);
                     const float top = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
                     corr[r] = 1.f;
-                    if (top > mref[r] + Threshold<EB>::v) {
+                    if (top > mref[r] + RaiseAbove<EB>::v) {
                         if (mref[r] != -INFINITY) {
                             corr[r] = fast_exp2(mref[r] - top);
                             rescale = true;
@@ -492,22 +483,23 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 // a row that saw nothing yet has no reference: every slot of it is masked
-                sv[r] = sv[r] == -INFINITY ? 0.f : fast_exp2(sv[r] - mref[r] + kOffset);
+                sv[r] = sv[r] == -INFINITY ? 0.f : fast_exp2(sv[r] - mref[r] + kWeightOffset);
                 lsum[r] = EB == 1 ? fmaf(sv[r], ivs, lsum[r]) : lsum[r] + sv[r];
             }
             if (c >= S::npt && !wait_pv(c - S::npt)) return;
             unsigned char* pb = pt + (c % S::npt) * S::pbytes;
             if (EB == 1) {
 #pragma unroll
-                for (int r = 0; r < NR; r += 2) {
-                    uint32_t hi, lo;
-                    split_weights(sv[r], sv[r + 1], hi, lo);
-                    unsigned char* o0 = pb + r * 128 + (((t >> 4) ^ (r & 7)) << 4) + (t & 15);
-                    unsigned char* o1 = pb + (r + 1) * 128 + (((t >> 4) ^ ((r + 1) & 7)) << 4) + (t & 15);
-                    o0[0] = static_cast<unsigned char>(hi);
-                    o1[0] = static_cast<unsigned char>(hi >> 8);
-                    o0[S::nblk] = static_cast<unsigned char>(lo);
-                    o1[S::nblk] = static_cast<unsigned char>(lo >> 8);
+                for (int r = 0; r < NR; r += 4) {
+                    uint32_t part[3];
+                    split_weights(sv[r], sv[r + 1], sv[r + 2], sv[r + 3], part);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        unsigned char* o = pb + (r + e) * 128 + (((t >> 4) ^ ((r + e) & 7)) << 4) + (t & 15);
+#pragma unroll
+                        for (int k2 = 0; k2 < 3; ++k2)
+                            o[k2 * S::nblk] = static_cast<unsigned char>(part[k2] >> (8 * e));
+                    }
                 }
             } else {
 #pragma unroll

@@ -8,17 +8,17 @@
 //   O += P V      (A = P from tensor memory, B = V tile read N-major)
 //
 // With 8-bit pools both products take the tiles as they lie in memory, the
-// query rows as two e4m3 parts and the weights as e4m3 + e5m2 (the same split,
-// scales and references as in kvc_paged_decode.cu): two products at twice
-// the 16-bit rate each, so the tensor-core time is that of 16-bit tiles, with half
-// the memory traffic and no conversion of the cache.
+// query rows as two e4m3 parts and the weights as three e5m2 parts (splits, scales
+// and references as in kvc_paged_decode.cu): five products at twice the 16-bit
+// rate against four halves, so the tensor-core time is 5/4 of 16-bit tiles', with
+// half the memory traffic and no conversion of the cache.
 //
 // The softmax, not the products, is the longer part of a tile: two groups of 4
 // warps take alternate tiles, each with its own S, O and row statistics, so
 // that one group's softmax runs under the other's products; at a run's end the two
 // halves of a row are joined out of tensor memory. P overwrites its S in place:
-// the 32 slots' weights of a K step lie in columns 16 i .. 16 i + 15 (8 for each
-// part), behind the columns still to be read.
+// the weights of 32 slots take 24 columns (16 of 16-bit weights), behind the 32
+// score columns that are read next.
 //
 // Tensor memory: S at columns 0 and 128, O at 256 and 384. Warps: 8 softmax, an S
 // issuer, a P.V issuer, a producer, and 4 that schedule the block's runs
@@ -34,13 +34,7 @@ namespace {
 constexpr int kTS = 128, kRows = 128;
 constexpr int kSWarp = 8, kPvWarp = 9, kProdWarp = 10, kQWarp = 12;  // 12..15: query rows
 constexpr int kThreads = 16 * 32;
-constexpr float kOffset = 7.f;  // weights are 2^(s - ref + 7)
 constexpr uint32_t kColS = 0, kColO = 256;
-
-template <int EB>
-struct Threshold {
-    static constexpr float v = EB == 1 ? 1.75f : 8.f;
-};
 
 struct Bars {
     uint32_t base;
@@ -279,10 +273,10 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
 #pragma unroll
                 for (int i = 0; i < 4; ++i)  // 32 slots per step
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        tc_mma_f8_ts(tO, tP + 16 * i + 8 * part,
+                    for (int part = 0; part < 3; ++part)
+                        tc_mma_f8_ts(tO, tP + 24 * i + 8 * part,
                                      smem_desc_sw128(sV + i * 32 * 128, 16, 1024),
-                                     mma_idesc_f8(kRows, N, part != 0, a.e5m2, false, true),
+                                     mma_idesc_f8(kRows, N, true, a.e5m2, false, true),
                                      n >= 2 || (i | part) != 0);
             } else {
 #pragma unroll
@@ -299,6 +293,13 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
     tc_commit(bars.drained());
     volatile int never = 0;
     mbar_wait(bars.drained(), 0u, &never);
+}
+
+// Columns past hi, and up to lo, masked.
+__device__ __forceinline__ void hide_columns(float (&s)[32], int hi, int lo) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i > hi || i <= lo) s[i] = -INFINITY;
 }
 
 template <typename T, int EB, bool MOD>
@@ -354,63 +355,65 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             const int j0 = (it.tile0 + n) * kTS;
             const bool edge = j0 + kTS - 1 > it.first || (a.window > 0 && j0 <= it.last - a.window);
             const StageScales* sc = scales + c % kScaleRing;
-            float s[kTS];  // the row's scores of the tile, then its weights
-            tmem_ld128(tS, s);
-            if (MOD) {
-#pragma unroll
-                for (int e = 0; e < kTS; e += 8) {
-                    float f = mul, lv = 0.f;
-                    if (EB == 1) {
-                        const float4 kv = sc->kv[e >> box];
-                        f *= kv.x;
-                        lv = kv.z;
-                    }
-                    if (a.softcap > 0.f) {
-                        // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-                        f *= cap_in;
-#pragma unroll
-                        for (int i = e; i < e + 8; ++i)
-                            s[i] = fmaf(-2.f * cap_out, fast_rcp(1.f + fast_exp2(s[i] * f)),
-                                        cap_out + lv);
-                    } else {
-                        f *= kLog2e;
-#pragma unroll
-                        for (int i = e; i < e + 8; ++i) s[i] = fmaf(s[i], f, lv);
-                    }
-                    if (a.slopes) {
-                        const float far = slope * static_cast<float>(lim - j0 - e);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            s[e + i] += fmaf(slope, static_cast<float>(i), -far);
-                    }
-                }
-            }
-            if (edge) {
-                const int hi = lim - j0, lo = low - j0;
-#pragma unroll
-                for (int i = 0; i < kTS; ++i)
-                    if (i > hi || i <= lo) s[i] = -INFINITY;
-            }
+            // first pass: the row's largest score of the tile; with a cap or a bias
+            // the scores go back to tensor memory. Both passes are loops of 32
+            // columns: unrolled whole, their code would not fit the instruction cache
             float top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                float s[32];
+                tmem_ld32(tS + 32 * q, s);
+                if (MOD) {
 #pragma unroll
-            for (int e = 0; e < kTS; e += 8) {
-                float m = fmaxf(fmaxf(s[e], s[e + 1]), s[e + 2]);
-                m = fmaxf(fmaxf(m, s[e + 3]), s[e + 4]);
-                m = fmaxf(fmaxf(m, s[e + 5]), s[e + 6]);
-                m = fmaxf(m, s[e + 7]);
-                if (!MOD) {
-                    float f = mul, lv = 0.f;
-                    if (EB == 1) {
-                        const float4 kv = sc->kv[e >> box];
-                        f = fmaxf(f * kv.x, 1e-37f);
-                        lv = kv.z;
+                    for (int e = 0; e < 32; e += 8) {
+                        float f = mul, lv = 0.f;
+                        if (EB == 1) {
+                            const float4 kv = sc->kv[(32 * q + e) >> box];
+                            f *= kv.x;
+                            lv = kv.z;
+                        }
+                        if (a.softcap > 0.f) {
+                            // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+                            f *= cap_in;
+#pragma unroll
+                            for (int i = e; i < e + 8; ++i)
+                                s[i] = fmaf(-2.f * cap_out, fast_rcp(1.f + fast_exp2(s[i] * f)),
+                                            cap_out + lv);
+                        } else {
+                            f *= kLog2e;
+#pragma unroll
+                            for (int i = e; i < e + 8; ++i) s[i] = fmaf(s[i], f, lv);
+                        }
+                        if (a.slopes) {
+                            const float far = slope * static_cast<float>(lim - j0 - 32 * q - e);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                s[e + i] += fmaf(slope, static_cast<float>(i), -far);
+                        }
                     }
-                    m = fmaf(m, f, lv);
                 }
-                top = fmaxf(top, m);
+                if (edge) hide_columns(s, lim - j0 - 32 * q, low - j0 - 32 * q);
+                if (MOD) tmem_st32(tS + 32 * q, s);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float m = fmaxf(fmaxf(s[e], s[e + 1]), s[e + 2]);
+                    m = fmaxf(fmaxf(m, s[e + 3]), s[e + 4]);
+                    m = fmaxf(fmaxf(m, s[e + 5]), s[e + 6]);
+                    m = fmaxf(m, s[e + 7]);
+                    if (!MOD) {
+                        float f = mul, lv = 0.f;
+                        if (EB == 1) {
+                            const float4 kv = sc->kv[(32 * q + e) >> box];
+                            f = fmaxf(f * kv.x, 1e-37f);
+                            lv = kv.z;
+                        }
+                        m = fmaf(m, f, lv);
+                    }
+                    top = fmaxf(top, m);
+                }
             }
             float corr = 1.f;
-            if (top > ref + Threshold<EB>::v) {
+            if (top > ref + RaiseAbove<EB>::v) {
                 corr = ref == -INFINITY ? 0.f : fast_exp2(ref - top);
                 l *= corr;
                 ref = top;
@@ -430,11 +433,14 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             }
             any = true;
             // the weights, over the scores (a row that saw nothing yet: all 2^-inf)
-            const float off = ref == -INFINITY ? kOffset : kOffset - ref;
+            const float off = ref == -INFINITY ? kWeightOffset : kWeightOffset - ref;
             float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < 4; ++q) {
-                uint32_t w[16];
+                float s[32];
+                tmem_ld32(tS + 32 * q, s);
+                if (!MOD && edge) hide_columns(s, lim - j0 - 32 * q, low - j0 - 32 * q);
+                uint32_t w[EB == 1 ? 24 : 16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     float f = MOD ? 1.f : mul, lv = off, ivs = 1.f;
@@ -447,7 +453,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                         ivs = kv.w;
                         sum = make_float2(0.f, 0.f);
                     }
-                    float* x = s + 32 * q + e;
+                    float* x = s + e;
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         const float2 v = fma2(make_float2(x[i], x[i + 1]), make_float2(f, f),
@@ -460,23 +466,22 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                         l = fmaf(sum.x + sum.y, ivs, l);
 #pragma unroll
                         for (int i = 0; i < 8; i += 4) {
-                            uint32_t h0, l0, h1, l1;
-                            split_weights(x[i], x[i + 1], h0, l0);
-                            split_weights(x[i + 2], x[i + 3], h1, l1);
-                            w[(e + i) / 4] = h0 | (h1 << 16);
-                            w[8 + (e + i) / 4] = l0 | (l1 << 16);
+                            uint32_t part[3];
+                            split_weights(x[i], x[i + 1], x[i + 2], x[i + 3], part);
+#pragma unroll
+                            for (int k2 = 0; k2 < 3; ++k2) w[8 * k2 + (e + i) / 4] = part[k2];
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack2<T>(x[i], x[i + 1]);
                     }
                 }
-                float wf[16];
+                constexpr int kWords = EB == 1 ? 24 : 16;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) wf[i] = __uint_as_float(w[i]);
-                tmem_stn<16>(tS + 16 * q, wf);
+                for (int i = 0; i < kWords; i += 8) tmem_st8_async(tS + kWords * q + i, w + i);
             }
             if (EB == 2) l += sum.x + sum.y;
+            tmem_wait_st();
             if (edge) {  // thread r looks after slot r's value row
                 if (!warp_wait(bars.v_full(stage), sph, abort)) return;
                 const int j = j0 + r;
@@ -637,13 +642,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemSlot);
     launch_dependents();
 
-    // the softmax threads keep a tile's row in registers: 192 each, 64 for the others
-    // (8 warps x 192 + 8 x 64 = the launch's 16 x 128)
+    // 184 registers for a softmax thread, 72 for the others (8 warps x 184 + 8 x 72 =
+    // the launch's 16 x 128)
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         softmax_warps<T, EB, MOD>(p, smem, bars, abort, tmem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kSWarp) {
             if ((threadIdx.x & 31) == 0) s_issuer<T, EB>(p, smem, bars, abort, tmem);
         } else if (warp == kPvWarp) {

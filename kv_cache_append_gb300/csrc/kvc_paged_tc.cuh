@@ -359,14 +359,38 @@ __device__ __forceinline__ void split_row_part(const float (&x)[4], float f, uin
         lo |= to_eight2<false>(u - hf.x, v - hf.y) << (8 * e);
     }
 }
-// Two weights (up to 448) as hi (e4m3) + lo (e5m2), by way of fp16, in which
-// the difference is exact.
-__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const __half2 w = __floats2half2_rn(a, b);
-    hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(w), __NV_SATFINITE, __NV_E4M3);
-    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(w, h)), __NV_SATFINITE, __NV_E5M2);
+// Four weights as three e5m2 parts each (a word of four codes per part). e5m2
+// is the upper byte of fp16, so from the weights in fp16 the first two parts are
+// cut off by a mask, each difference is exact, and the last is rounded: 3 + 3 + 3
+// significant bits. A weight from 2^-8 to 2^15.75 is off by at most 2^-9 of
+// itself (and fp16's 2^-12), any other by 2^-17.
+__device__ __forceinline__ void split_weights(float a, float b, float c, float d, uint32_t* part) {
+    const __half2 w0 = __floats2half2_rn(a, b), w1 = __floats2half2_rn(c, d);
+    const uint32_t m = 0xff00ff00u;
+    const uint32_t u0 = *reinterpret_cast<const uint32_t*>(&w0);
+    const uint32_t u1 = *reinterpret_cast<const uint32_t*>(&w1);
+    const uint32_t h0 = u0 & m, h1 = u1 & m;
+    const __half2 r0 = __hsub2(w0, *reinterpret_cast<const __half2*>(&h0));
+    const __half2 r1 = __hsub2(w1, *reinterpret_cast<const __half2*>(&h1));
+    const uint32_t v0 = *reinterpret_cast<const uint32_t*>(&r0);
+    const uint32_t v1 = *reinterpret_cast<const uint32_t*>(&r1);
+    const uint32_t g0 = v0 & m, g1 = v1 & m;
+    const __half2 q0 = __hsub2(r0, *reinterpret_cast<const __half2*>(&g0));
+    const __half2 q1 = __hsub2(r1, *reinterpret_cast<const __half2*>(&g1));
+    part[0] = __byte_perm(u0, u1, 0x7531);
+    part[1] = __byte_perm(v0, v1, 0x7531);
+    part[2] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(q0), __NV_SATFINITE, __NV_E5M2) |
+              (static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(q1),
+                                                                __NV_SATFINITE, __NV_E5M2)) << 16);
 }
+// Of the 8-bit kernels a weight is 2^(s - ref + 8), and a row's reference is
+// raised when a score exceeds it by more than 7.75: weights stay under e5m2's
+// largest, 57344. 16-bit weights have the room of fp16 above 2^8.
+constexpr float kWeightOffset = 8.f;
+template <int EB>
+struct RaiseAbove {
+    static constexpr float v = EB == 1 ? 7.75f : 7.f;
+};
 
 // A word of 8- or 16-bit elements with those that are an infinity or NaN cleared.
 template <int EB, typename T>

@@ -66,7 +66,7 @@ def check(x, got, max_q, scale=None, softcap=0.0, slopes=None, window=0, rows=No
     assert (err <= bound)[live].all(), f"{float(worst.max()):.3g} times the bound"
     if telling:
         # the bound takes every rounding at its worst; over a whole result they
-        # are independent, and its relative error is about that of one weight (2^-7 at
+        # are independent, and its relative error is about that of one weight (2^-8 at
         # most) and one score (2^-8 of a term, D of them of either sign)
         rel = float(err[live].norm() / want[live].norm())
         assert rel < (1e-5 if x["q"].dtype == torch.float32 else 2e-2), rel
