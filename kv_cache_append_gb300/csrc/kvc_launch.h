@@ -223,6 +223,7 @@ struct PagedTcParams {
     PagedAttendParams a;
     int RG;            // query rows of a unit
     int ctas;          // blocks of the grid
+    uint32_t bs_mul, bs_shift;  // slot / block_size = slot * bs_mul >> bs_shift (slots below 2^30)
     int hh;            // slots of a box: the largest power of two up to 128 dividing block_size
     int ns, ni;        // stages (rows kernel: of keys), item and query buffers
     int nv;            // rows kernel: stages of values
@@ -231,6 +232,10 @@ struct PagedTcParams {
     float* part_ml;    // [2 ctas][RG][2]
     float* part_acc;   // [2 ctas][RG][Dv]
     PagedRec* rec;     // [ctas]
+
+    __device__ __forceinline__ int block_of(int slot) const {
+        return static_cast<int>((static_cast<uint64_t>(slot) * bs_mul) >> bs_shift);
+    }
 };
 // Units of up to 32 query rows; nr: 4, 8, 16 or 32 (>= the rows of a unit).
 cudaError_t launch_paged_decode(const PagedTcParams& p, int dtype, int pool_dtype, int nr,

@@ -108,6 +108,12 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         return t;
     std::memset(&t.p, 0, sizeof(t.p));
     PagedTcParams& p = t.p;
+    // exact for slots below 2^30: with l = ceil(log2 d), m = ceil(2^(30 + l) / d), the
+    // excess m d - 2^(30 + l) < d <= 2^l takes slot m / 2^(30 + l) less than 1 / d up
+    int l = 0;
+    while ((int64_t(1) << l) < d.block_size) ++l;
+    p.bs_shift = static_cast<uint32_t>(30 + l);
+    p.bs_mul = static_cast<uint32_t>(((int64_t(1) << (30 + l)) + d.block_size - 1) / d.block_size);
     if (R > 32) {
         // groups of 128 rows: query buffers, then rings of key and value tiles
         const int64_t parts = es == 1 ? 2 : 1, nkb = (d.D * es + 127) / 128, nvb = (d.Dv * es + 127) / 128;
@@ -115,7 +121,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         p.RG = 128;
         p.hh = 128;
         while (d.block_size % p.hh != 0) p.hh /= 2;
-        p.off_q = es == 1 ? 7168 : 3072;  // scales of 16 tiles, or none
+        p.off_q = es == 1 ? 12288 : 8192;  // scales of 16 tiles, or none
         p.q_bytes = static_cast<int>(parts * kb + (es == 1 ? 1024 : 0));
         // the next run's query rows are prepared ahead where that leaves three tiles
         int64_t room = kSmemBlock - p.off_q - 2 * p.q_bytes;

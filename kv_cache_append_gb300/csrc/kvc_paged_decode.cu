@@ -206,20 +206,30 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
         if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
         const PagedItem it = items[kb];
         if (it.flags & kItemDone) break;
+        int id = feed_id<kTS>(p, it, it.tile0);
+        int id1 = it.nt > 1 ? feed_id<kTS>(p, it, it.tile0 + 1) : kNoBox;
+        float2 fs = make_float2(1.f, 1.f), fs1 = fs;
+        if (EB == 1) fs = feed_scales(p, it, id);
         for (int n = 0; n < it.nt; ++n) {
+            const int tile = it.tile0 + n;
+            const int id2 = n + 2 < it.nt ? feed_id<kTS>(p, it, tile + 2) : kNoBox;
+            if (EB == 1) fs1 = feed_scales(p, it, id1);
             if (issued >= p.ns && !warp_wait(bars.empty(ring.s), ring.ph ^ 1u, abort)) {
                 ok = false;
                 break;
             }
-            const uint32_t sK = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes;
-            const uint32_t sV = sK + static_cast<uint32_t>(nkb * kTS * 128);
-            const PagedBoxes x = paged_boxes<EB, kTS>(p, it, it.tile0 + n, sc + ring.s);
-            paged_load_boxes<EB, kTS>(p, &p.tk, x, sK, nkb, bars.full(ring.s), true, nvb);
-            paged_load_boxes<EB, kTS>(p, &p.tv, x, sV, nvb, bars.full(ring.s), false);
-            if (x.bad && lane == 0) {
+            if (__any_sync(0xffffffffu, feed_bad(p, id)) && lane == 0) {
                 *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 1;
                 if (a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
             }
+            if (EB == 1) feed_store(sc + ring.s, fs);
+            const uint32_t sK = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes;
+            feed_copy<EB, kTS>(p, it, &p.tk, tile, id, sK, nkb, bars.full(ring.s), true, nvb);
+            feed_copy<EB, kTS>(p, it, &p.tv, tile, id, sK + static_cast<uint32_t>(nkb * kTS * 128), nvb,
+                               bars.full(ring.s), false);
+            id = id1;
+            id1 = id2;
+            fs = fs1;
             ++issued;
             ring.next(p.ns);
         }

@@ -13,16 +13,20 @@
 // rate against four halves, so the tensor-core time is 5/4 of 16-bit tiles', with
 // half the memory traffic and no conversion of the cache.
 //
-// The softmax, not the products, is the longer part of a tile: two groups of 4
-// warps take alternate tiles, each with its own S, O and row statistics, so
-// that one group's softmax runs under the other's products; at a run's end the two
-// halves of a row are joined out of tensor memory. P overwrites its S in place:
-// the weights of 32 slots take 24 columns (16 of 16-bit weights), behind the 32
-// score columns that are read next.
+// The softmax, not the products, is the longer part of a tile, and a tile's chain
+// (S, softmax, P V, the next S into the same columns) is longer still: three groups
+// of 4 warps take the tiles in turn, each with its S in tensor memory, so that
+// two tiles' softmax run under one tile's products and barriers. O is one for all of them,
+// so a row has one reference: tile n's warp reads what tile n - 1's warp of the
+// same rows left before it makes its weights (a decision comes after the first of a
+// tile's two passes, and raising is rare), and each group measures its sum by the
+// reference it last saw. P overwrites its S in place: the weights of 32 slots take 24
+// columns (16 of 16-bit weights), behind the 32 score columns that are read next.
 //
-// Tensor memory: S at columns 0 and 128, O at 256 and 384. Warps: 8 softmax, an S
-// issuer, a P.V issuer, a producer, and 4 that schedule the block's runs
-// (kvc_paged_tc.cuh) and prepare the next run's query rows.
+// Tensor memory: S of the groups at columns 0, 128 and 256, O at 384. Warps: 12
+// softmax, an S issuer, a P.V issuer, a producer of key tiles and one of value tiles,
+// and 4 that schedule the block's runs (kvc_paged_tc.cuh) and prepare the next
+// run's query rows.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,9 +36,11 @@ namespace kvc {
 namespace {
 
 constexpr int kTS = 128, kRows = 128;
-constexpr int kSWarp = 8, kPvWarp = 9, kProdWarp = 10, kQWarp = 12;  // 12..15: query rows
-constexpr int kThreads = 16 * 32;
-constexpr uint32_t kColS = 0, kColO = 256;
+constexpr int kGroups = 3;                 // of 4 softmax warps, tiles in turn
+constexpr int kSoft = 4 * kGroups;
+constexpr int kSWarp = 12, kPvWarp = 13, kKWarp = 14, kVWarp = 15, kQWarp = 16;  // 16..19: query rows
+constexpr int kThreads = 20 * 32;
+constexpr uint32_t kColS = 0, kColO = 384;  // S buffers of the three groups, O
 
 struct Bars {
     uint32_t base;
@@ -45,15 +51,33 @@ struct Bars {
     __device__ uint32_t item_full(int k) const { return base + 256u + 8u * k; }
     __device__ uint32_t item_empty(int k) const { return base + 272u + 8u * k; }
     __device__ uint32_t s_ready(int g) const { return base + 288u + 8u * g; }
-    __device__ uint32_t p_ready(int g) const { return base + 304u + 8u * g; }
-    __device__ uint32_t o_done(int g) const { return base + 320u + 8u * g; }
-    __device__ uint32_t meet() const { return base + 336u; }
-    __device__ uint32_t o_free() const { return base + 344u; }
-    __device__ uint32_t drained() const { return base + 352u; }
+    __device__ uint32_t p_ready(int g) const { return base + 312u + 8u * g; }
+    __device__ uint32_t o_done(int g) const { return base + 336u + 8u * g; }
+    // per 32 rows and group: one barrier for all would let a group that is two tiles
+    // ahead of the decisions take an old phase for the one it waits for
+    __device__ uint32_t decide(int w, int g) const { return base + 360u + 8u * (3 * w + g); }
+    __device__ uint32_t meet() const { return base + 456u; }
+    __device__ uint32_t o_free() const { return base + 464u; }
+    __device__ uint32_t drained() const { return base + 472u; }
 };
-constexpr int kTmemSlot = 360, kAbort = 364, kBad = 368 /* [2] */, kOdd = 376 /* [2] */;
-constexpr int kStart = 512, kItems = 896, kXml = 1024;  // 2 KB of exchanged row statistics
-constexpr int kScales = 3072, kScaleRing = 16;          // 8-bit pools: 16 tiles' scales
+constexpr int kTmemSlot = 480, kAbort = 484, kBad = 488 /* [2] */, kOdd = 496 /* [2] */;
+constexpr int kStart = 512, kItems = 896;
+// exchanged between the groups, for even and odd runs: a row's reference [2][128],
+// each group's sum and the reference it is measured by [2][3][128]
+constexpr int kXr = 1024, kXl = 2048;
+constexpr int kScales = 8192, kScaleRing = 16;  // 8-bit pools: 16 tiles' scales
+
+// Tile c's group (c % 3) and the parity of its use of that group's barriers.
+struct Turn {
+    int g = 0;
+    uint32_t ph = 0;
+    __device__ void next() {
+        if (++g == kGroups) {
+            g = 0;
+            ph ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ void tc_mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                              uint32_t idesc, bool accumulate) {
@@ -136,7 +160,8 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
     }
 }
 
-template <int EB>
+// Two warps: the key tiles (with the scales) and the value tiles.
+template <int EB, bool KEYS>
 __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars bars,
                               volatile int* abort) {
     const PagedAttendParams& a = p.a;
@@ -144,47 +169,52 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + kItems);
     StageScales* sc = reinterpret_cast<StageScales*>(smem + kScales);
     const int nkb = (a.D * EB + 127) / 128, nvb = (a.Dv * EB + 127) / 128;
-    const uint32_t sK = smem_addr(smem + p.off_stage), kbytes = nkb * kTS * 128;
-    const uint32_t sV = sK + p.ns * kbytes, vbytes = nvb * kTS * 128;
-    int ck = 0, cv = 0;  // key and value tiles issued
-    Ring kr, vr;
+    const int nb = KEYS ? nkb : nvb, stages = KEYS ? p.ns : p.nv;
+    const uint32_t bytes = nb * kTS * 128;
+    const uint32_t base = smem_addr(smem + p.off_stage) + (KEYS ? 0 : p.ns * nkb * kTS * 128);
+    int c = 0;  // tiles issued
+    Ring ring;
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
         if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
         const PagedItem it = items[kb];
         if (it.flags & kItemDone) break;
+        constexpr bool kScaled = EB == 1 && KEYS;
+        int id = feed_id<kTS>(p, it, it.tile0);
+        int id1 = it.nt > 1 ? feed_id<kTS>(p, it, it.tile0 + 1) : kNoBox;
+        float2 fs = make_float2(1.f, 1.f), fs1 = fs;
+        if (kScaled) fs = feed_scales(p, it, id);
         for (int n = 0; n < it.nt; ++n) {
-            if (ck >= p.ns && !warp_wait(bars.k_empty(kr.s), kr.ph ^ 1u, abort)) {
+            const int tile = it.tile0 + n;
+            const int id2 = n + 2 < it.nt ? feed_id<kTS>(p, it, tile + 2) : kNoBox;
+            if (kScaled) fs1 = feed_scales(p, it, id1);
+            if (c >= stages &&
+                !warp_wait(KEYS ? bars.k_empty(ring.s) : bars.v_empty(ring.s), ring.ph ^ 1u, abort)) {
                 ok = false;
                 break;
             }
-            const PagedBoxes x = paged_boxes<EB, kTS>(p, it, it.tile0 + n, sc + ck % kScaleRing);
-            if (x.bad && lane == 0) {
+            if (KEYS && __any_sync(0xffffffffu, feed_bad(p, id)) && lane == 0) {
                 *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 1;
                 if (a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
             }
-            paged_load_boxes<EB, kTS>(p, &p.tk, x, sK + kr.s * kbytes, nkb, bars.k_full(kr.s));
-            ++ck;
-            kr.next(p.ns);
-            if (cv >= p.nv && !warp_wait(bars.v_empty(vr.s), vr.ph ^ 1u, abort)) {
-                ok = false;
-                break;
-            }
-            paged_load_boxes<EB, kTS>(p, &p.tv, x, sV + vr.s * vbytes, nvb, bars.v_full(vr.s));
-            ++cv;
-            vr.next(p.nv);
+            if (kScaled) feed_store(sc + c % kScaleRing, fs);
+            feed_copy<EB, kTS>(p, it, KEYS ? &p.tk : &p.tv, tile, id, base + ring.s * bytes, nb,
+                               KEYS ? bars.k_full(ring.s) : bars.v_full(ring.s));
+            id = id1;
+            id1 = id2;
+            fs = fs1;
+            ++c;
+            ring.next(stages);
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bars.item_empty(kb), 1u);
     }
     // do not leave while issued copies may still write shared memory
-    if (lane == 0) {
-        for (int q = ck > p.ns ? ck - p.ns : 0; q < ck; ++q)
-            mbar_drain(bars.k_full(q % p.ns), static_cast<uint32_t>((q / p.ns) & 1));
-        for (int q = cv > p.nv ? cv - p.nv : 0; q < cv; ++q)
-            mbar_drain(bars.v_full(q % p.nv), static_cast<uint32_t>((q / p.nv) & 1));
-    }
+    if (lane == 0)
+        for (int q = c > stages ? c - stages : 0; q < c; ++q)
+            mbar_drain(KEYS ? bars.k_full(q % stages) : bars.v_full(q % stages),
+                       static_cast<uint32_t>((q / stages) & 1));
 }
 
 // One thread: S of every tile, into its group's buffer once the group's last
@@ -201,6 +231,7 @@ __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars,
                                    : mma_idesc_f16(kRows, kTS, std::is_same<T, __nv_bfloat16>::value,
                                                    false, false);
     Ring kr;
+    Turn turn;
     int c = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -210,27 +241,36 @@ __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars,
         const int nt = items[kb].nt;
         const uint32_t sQ = smem_addr(smem + p.off_q + kb * p.q_bytes);
         for (int n = 0; n < nt; ++n, ++c) {
-            const int g = c & 1;
+            const int g = turn.g;
             if (!mbar_wait(bars.k_full(kr.s), kr.ph, abort) ||
-                (c >= 2 && !mbar_wait(bars.o_done(g), static_cast<uint32_t>((c / 2 - 1) & 1), abort))) {
+                (c >= kGroups && !mbar_wait(bars.o_done(g), turn.ph ^ 1u, abort))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const uint32_t sK = sK0 + kr.s * nkb * kTS * 128;
-            for (int part = 0; part < kParts; ++part)
-                for (int i = 0; i < ksteps; ++i) {
-                    const uint64_t da = smem_desc_sw128(
-                        sQ + (part * nkb + (i >> 2)) * kBlk + (i & 3) * 32, 16, 1024);
-                    const uint64_t db = smem_desc_sw128(sK + (i >> 2) * kTS * 128 + (i & 3) * 32, 16, 1024);
-                    if (EB == 1)
-                        tc_mma_f8(tmem + kColS + 128 * g, da, db, idesc, (part | i) != 0);
-                    else
-                        tc_mma(tmem + kColS + 128 * g, da, db, idesc, i != 0);
+            const uint32_t tS = tmem + kColS + 128 * g;
+            for (int b = 0; b < nkb; ++b) {
+                // column block b of both; 32 bytes of a row per instruction, 2 in the
+                // descriptor's address field
+                const uint64_t db = smem_desc_sw128(sK + b * kTS * 128, 16, 1024);
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+                    const uint64_t da = smem_desc_sw128(sQ + (part * nkb + b) * kBlk, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (4 * b + i >= ksteps) break;
+                        if (EB == 1)
+                            tc_mma_f8(tS, da + 2 * i, db + 2 * i, idesc, (b | part | i) != 0);
+                        else
+                            tc_mma(tS, da + 2 * i, db + 2 * i, idesc, (b | i) != 0);
+                    }
                 }
+            }
             tc_commit(bars.s_ready(g));
             tc_commit(bars.k_empty(kr.s));
             kr.next(p.ns);
+            turn.next();
         }
         if (ok) tc_commit(bars.item_empty(kb));  // once the products have read the query rows
     }
@@ -248,9 +288,10 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
     const int nkb = (a.D * EB + 127) / 128, nvb = (a.Dv * EB + 127) / 128;
     const uint32_t sV0 = smem_addr(smem + p.off_stage) + p.ns * nkb * kTS * 128;
     const int N = (a.Dv + 15) / 16 * 16;
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t idesc = EB == 1 ? mma_idesc_f8(kRows, N, true, a.e5m2, false, true)
+                                   : mma_idesc_f16(kRows, N, std::is_same<T, __nv_bfloat16>::value, true);
     Ring vr;
-    int c = 0;
+    Turn turn;
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
@@ -259,40 +300,45 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
         const int nt = items[kb].nt;
         // the last run's O has been read
         if (k > 0 && !mbar_wait(bars.o_free(), static_cast<uint32_t>((k - 1) & 1), abort)) break;
-        for (int n = 0; n < nt; ++n, ++c) {
-            const int g = c & 1;
+        for (int n = 0; n < nt; ++n) {
+            const int g = turn.g;
             if (!mbar_wait(bars.v_full(vr.s), vr.ph, abort) ||
-                !mbar_wait(bars.p_ready(g), static_cast<uint32_t>((c / 2) & 1), abort)) {
+                !mbar_wait(bars.p_ready(g), turn.ph, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const uint32_t sV = sV0 + vr.s * nvb * kTS * 128;
-            const uint32_t tP = tmem + kColS + 128 * g, tO = tmem + kColO + 128 * g;
+            const uint32_t tP = tmem + kColS + 128 * g, tO = tmem + kColO;
+            const uint64_t dv = smem_desc_sw128(sV, kTS * 128, 1024);
             if (EB == 1) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)  // 32 slots per step
 #pragma unroll
                     for (int part = 0; part < 3; ++part)
                         tc_mma_f8_ts(tO, tP + 24 * i + 8 * part,
-                                     smem_desc_sw128(sV + i * 32 * 128, 16, 1024),
-                                     mma_idesc_f8(kRows, N, true, a.e5m2, false, true),
-                                     n >= 2 || (i | part) != 0);
+                                     dv + i * (32 * 128 / 16), idesc, (n | i | part) != 0);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)  // 16 slots per step
-                    tc_mma_ts(tO, tP + 8 * i, smem_desc_sw128(sV + i * 16 * 128, kTS * 128, 1024),
-                              mma_idesc_f16(kRows, N, kBf16, true), n >= 2 || i != 0);
+                    tc_mma_ts(tO, tP + 8 * i, dv + i * (16 * 128 / 16), idesc, (n | i) != 0);
             }
             tc_commit(bars.o_done(g));
             tc_commit(bars.v_empty(vr.s));
             vr.next(p.nv);
+            turn.next();
         }
         if (ok) mbar_arrive(bars.item_empty(kb), 1u);
     }
     tc_commit(bars.drained());
     volatile int never = 0;
     mbar_wait(bars.drained(), 0u, &never);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Columns past hi, and up to lo, masked.
@@ -308,21 +354,20 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
     using St = Storage<T>;
     const PagedAttendParams& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = warp >> 2;
+    const int g = warp >> 2, wq = warp & 3;
     const int r = threadIdx.x & 127;  // query row (tensor-memory lane)
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lanes + kColS + 128 * g, tO = tmem + lanes + kColO;
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + kItems);
     const StageScales* scales = reinterpret_cast<const StageScales*>(smem + kScales);
-    float2* xml = reinterpret_cast<float2*>(smem + kXml);  // [2][128] (reference, sum)
     const int nkb = (a.D * EB + 127) / 128, nvb = (a.Dv * EB + 127) / 128;
     const int box = 31 - __clz(p.hh);
     unsigned char* sV0 = smem + p.off_stage + p.ns * nkb * kTS * 128;
     const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
     const float cap_out = a.softcap * kLog2e;
-    int c = 0;       // tiles so far, both groups'
-    int vs = 0;      // value stage of tile c
-    uint32_t vph = 0;
+    int c = 0;      // tiles so far, all groups'
+    Turn turn;      // tile c's group
+    Ring vr;        // and value stage
 
     for (int k = 0;; ++k) {
         const int kb = k % p.ni;
@@ -340,17 +385,18 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         if (EB == 1)
             mul = reinterpret_cast<const float*>(smem + p.off_q + kb * p.q_bytes + 2 * nkb * kRows * 128)[r];
         if (!MOD) mul *= kLog2e;
-        float ref = -INFINITY, l = 0.f;
-        bool any = false;  // this group has had a tile of the run
+        // the row's reference is one for all groups: tile n's warp reads what tile n -
+        // 1's left, and may raise it
+        float* xr = reinterpret_cast<float*>(smem + kXr) + (k & 1) * 128 + r;
+        float2* xl = reinterpret_cast<float2*>(smem + kXl) + (k & 1) * 3 * 128 + r;
+        float ref = -INFINITY, l = 0.f;  // the reference that this group's sum is measured by
         for (int n = 0; n < it.nt; ++n, ++c) {
-            const int stage = vs;
-            const uint32_t sph = vph;
-            if (++vs == p.nv) {
-                vs = 0;
-                vph ^= 1u;
-            }
-            if ((c & 1) != g) continue;
-            if (!warp_wait(bars.s_ready(g), static_cast<uint32_t>((c / 2) & 1), abort)) return;
+            const int stage = vr.s, tg = turn.g;
+            const uint32_t sph = vr.ph, tph = turn.ph;
+            vr.next(p.nv);
+            turn.next();
+            if (tg != g) continue;
+            if (!warp_wait(bars.s_ready(g), tph, abort)) return;
             tc_fence_after();
             const int j0 = (it.tile0 + n) * kTS;
             const bool edge = j0 + kTS - 1 > it.first || (a.window > 0 && j0 <= it.last - a.window);
@@ -396,9 +442,9 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 if (MOD) tmem_st32(tS + 32 * q, s);
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
-                    float m = fmaxf(fmaxf(s[e], s[e + 1]), s[e + 2]);
-                    m = fmaxf(fmaxf(m, s[e + 3]), s[e + 4]);
-                    m = fmaxf(fmaxf(m, s[e + 5]), s[e + 6]);
+                    float m = max3(s[e], s[e + 1], s[e + 2]);
+                    m = max3(m, s[e + 3], s[e + 4]);
+                    m = max3(m, s[e + 5], s[e + 6]);
                     m = fmaxf(m, s[e + 7]);
                     if (!MOD) {
                         float f = mul, lv = 0.f;
@@ -412,26 +458,34 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                     top = fmaxf(top, m);
                 }
             }
-            float corr = 1.f;
-            if (top > ref + RaiseAbove<EB>::v) {
-                corr = ref == -INFINITY ? 0.f : fast_exp2(ref - top);
-                l *= corr;
-                ref = top;
+            // the last tile's decision, then this one's; a raised reference also
+            // rescales O, at rest between the two tiles' products
+            const int pg = g == 0 ? kGroups - 1 : g - 1;  // tile c - 1's group and parity
+            const uint32_t pph = g == 0 ? tph ^ 1u : tph;
+            if (n > 0 && !warp_wait(bars.decide(wq, pg), pph, abort)) return;
+            const float was = n > 0 ? *xr : -INFINITY;
+            const bool raise = top > was + RaiseAbove<EB>::v;
+            const float now = raise ? top : was;
+            if (n == 0 || raise) *xr = now;
+            const bool some = __any_sync(0xffffffffu, raise && was != -INFINITY);
+            if (lane == 0) mbar_arrive(bars.decide(wq, g), 1u);
+            if (now != ref) {
+                if (ref != -INFINITY) l *= fast_exp2(ref - now);
+                ref = now;
             }
-            if (__any_sync(0xffffffffu, corr != 1.f) && any) {
-                // O is at rest: S of this tile was issued after the group's last product
-                if (!warp_wait(bars.o_done(g), static_cast<uint32_t>((c / 2 - 1) & 1), abort)) return;
+            if (some) {
+                if (!warp_wait(bars.o_done(pg), pph, abort)) return;
                 tc_fence_after();
+                const float corr = raise && was != -INFINITY ? fast_exp2(was - now) : 1.f;
 #pragma unroll 1
                 for (int d = 0; d < a.Dv; d += 16) {
                     float o[16];
-                    tmem_ldn<16>(tO + 128 * g + d, o);
+                    tmem_ldn<16>(tO + d, o);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] *= corr;
-                    tmem_stn<16>(tO + 128 * g + d, o);
+                    tmem_stn<16>(tO + d, o);
                 }
             }
-            any = true;
             // the weights, over the scores (a row that saw nothing yet: all 2^-inf)
             const float off = ref == -INFINITY ? kWeightOffset : kWeightOffset - ref;
             float2 sum = make_float2(0.f, 0.f);
@@ -496,6 +550,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                                 make_uint4(0u, 0u, 0u, 0u);
                 } else if (!all) {
                     for (int b = 0; b < nvb; ++b)
+#pragma unroll 4
                         for (int i = 0; i < 32; ++i) {
                             uint32_t* x = reinterpret_cast<uint32_t*>(vrow + b * kTS * 128) +
                                           ((i + lane) & 31);
@@ -512,26 +567,23 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.p_ready(g), 1u);
         }
-        // the run's end: both groups' last products
-        // (a group without a tile of this run leaves the last run's to its readers)
-        if (any) xml[g * 128 + r] = make_float2(ref, l);
-        for (int h = 0; h < 2; ++h) {
-            const int done = (c + 1 - h) / 2;  // tiles of group h so far
-            if (done > 0 && !warp_wait(bars.o_done(h), static_cast<uint32_t>((done - 1) & 1), abort))
-                return;
+        // the run's end: its last product (the last tile is turn's predecessor)
+        xl[128 * g] = make_float2(l, ref);
+        {
+            const int pg = turn.g == 0 ? kGroups - 1 : turn.g - 1;
+            if (!warp_wait(bars.o_done(pg), turn.g == 0 ? turn.ph ^ 1u : turn.ph, abort)) return;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.meet(), 1u);
         if (!warp_wait(bars.meet(), static_cast<uint32_t>(k & 1), abort)) return;
         tc_fence_after();
-        const float2 x0 = xml[r], x1 = xml[128 + r];
-        const bool has0 = it.nt >= 2 || ((c - 1) & 1) == 0, has1 = it.nt >= 2 || ((c - 1) & 1) == 1;
-        const float m = fmaxf(has0 ? x0.x : -INFINITY, has1 ? x1.x : -INFINITY);
-        const float f0 = has0 ? (x0.x == m ? 1.f : fast_exp2(x0.x - m)) : 0.f;
-        const float f1 = has1 ? (x1.x == m ? 1.f : fast_exp2(x1.x - m)) : 0.f;
+        const float m = *xr;
         float sum = 0.f;
-        if (has0) sum = fmaf(x0.y, f0, sum);
-        if (has1) sum = fmaf(x1.y, f1, sum);
+#pragma unroll
+        for (int h = 0; h < kGroups; ++h) {
+            const float2 x = xl[128 * h];
+            if (x.x != 0.f) sum = fmaf(x.x, x.y == m ? 1.f : fast_exp2(x.y - m), sum);
+        }
         const bool bad = *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) != 0;
         const bool odds = *odd == k + 1;
         const bool whole = (it.flags & kItemBegins) && (it.flags & kItemEnds);
@@ -539,17 +591,11 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         const int64_t row = static_cast<int64_t>(it.q0 + (live ? rr / a.G : 0)) * a.Hq +
                             it.hk * a.G + (live ? rr % a.G : 0);
         const float inv = __fdiv_rn(1.f, sum);
-        // columns in runs of 16, the groups in turn
-        for (int d = 16 * g; d < a.Dv; d += 32) {
-            float o[16], o1[16];
-            if (has0) tmem_ldn<16>(tO + d, o);
-            if (has1) tmem_ldn<16>(tO + 128 + d, o1);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float v = has0 ? o[i] * f0 : 0.f;
-                if (has1) v = fmaf(o1[i], f1, v);
-                o[i] = v;
-            }
+        // columns in runs of 16, in turn
+#pragma unroll 1
+        for (int d = 16 * g; d < a.Dv; d += 16 * kGroups) {
+            float o[16];
+            tmem_ldn<16>(tO + d, o);
             if (odds && live) {  // what was cleared: from memory, into the rows that see it
                 const int j1 = min(lim, (it.tile0 + it.nt) * kTS - 1);
                 for (int j = max(low + 1, it.tile0 * kTS); j <= j1; ++j) {
@@ -619,13 +665,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(bars.item_full(k), 4u);         // the query warps
-            mbar_init(bars.item_empty(k), 3u + 8u);   // producer, both issuers, softmax warps
-            mbar_init(bars.s_ready(k), 1u);
-            mbar_init(bars.p_ready(k), 4u);
-            mbar_init(bars.o_done(k), 1u);
+            mbar_init(bars.item_empty(k), 4u + kSoft);  // producers, issuers, softmax warps
         }
-        mbar_init(bars.meet(), 8u);
-        mbar_init(bars.o_free(), 8u);
+        for (int g = 0; g < kGroups; ++g) {
+            mbar_init(bars.s_ready(g), 1u);
+            mbar_init(bars.p_ready(g), 4u);
+            mbar_init(bars.o_done(g), 1u);
+        }
+        for (int w = 0; w < 4; ++w)
+            for (int g = 0; g < kGroups; ++g) mbar_init(bars.decide(w, g), 1u);
+        mbar_init(bars.meet(), kSoft);
+        mbar_init(bars.o_free(), kSoft);
         mbar_init(bars.drained(), 2u);
         *abort = 0;
         *reinterpret_cast<volatile int*>(smem + kOdd) = 0;
@@ -642,19 +692,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemSlot);
     launch_dependents();
 
-    // 184 registers for a softmax thread, 72 for the others (8 warps x 184 + 8 x 72 =
-    // the launch's 16 x 128)
-    if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // 120 registers for a softmax thread, 56 for the others: 12 warps x 120 + 8 x 56 <=
+    // the launch's 20 x 96
+    if (warp < kSoft) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         softmax_warps<T, EB, MOD>(p, smem, bars, abort, tmem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kSWarp) {
             if ((threadIdx.x & 31) == 0) s_issuer<T, EB>(p, smem, bars, abort, tmem);
         } else if (warp == kPvWarp) {
             if ((threadIdx.x & 31) == 0) pv_issuer<T, EB>(p, smem, bars, abort, tmem);
-        } else if (warp == kProdWarp) {
-            producer_warp<EB>(p, smem, bars, abort);
+        } else if (warp == kKWarp) {
+            producer_warp<EB, true>(p, smem, bars, abort);
+        } else if (warp == kVWarp) {
+            producer_warp<EB, false>(p, smem, bars, abort);
         } else if (warp >= kQWarp) {
             query_warps<T, EB>(p, smem, bars, st, abort);
         }

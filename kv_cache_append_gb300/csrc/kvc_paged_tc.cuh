@@ -259,63 +259,54 @@ struct StageScales {
     float4 kv[kMaxBoxes];
 };
 
-// One tile's boxes (rows of one pool block each) that hold a visible slot: a
-// lane each. `bad`: a block id lies outside the pool (block 0 is read instead).
-struct PagedBoxes {
-    int pa, pb;  // boxes [pa, pb)
-    int y, z;    // this lane's box: its first row in the block, its pool unit
-    bool bad;
-};
-template <int EB, int TS>
-__device__ __forceinline__ PagedBoxes paged_boxes(const PagedTcParams& p, const PagedItem& it,
-                                                  int tile, StageScales* sc) {
-    const PagedAttendParams& a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int j0 = tile * TS, hh = p.hh;
-    PagedBoxes x;
-    x.pa = max(0, it.lo - j0) / hh;
-    x.pb = (min(TS, it.last + 1 - j0) + hh - 1) / hh;
-    int id = 0;
-    x.y = 0;
-    bool bad = false;
-    if (EB == 1 && lane < kMaxBoxes && (lane < x.pa || lane >= x.pb))
-        sc->kv[lane] = make_float4(1.f, 1.f, 0.f, 1.f);  // masked slots: anything finite
-    if (lane >= x.pa && lane < x.pb) {
-        const int slot = j0 + lane * hh, blk = slot / a.bs;
-        x.y = slot - blk * a.bs;
-        id = a.table[it.b * a.max_blocks + blk];
-        if (id < 0 || id >= a.num_blocks) {
-            bad = true;
-            id = 0;
-        }
-        if (EB == 1) {
-            const int64_t u = static_cast<int64_t>(id) * a.Hk + it.hk;
-            const float vs = a.vs[u];
-            sc->kv[lane] = make_float4(a.ks[u], vs, __log2f(vs), __fdiv_rn(1.f, vs));
-        }
-    }
-    x.z = id * a.Hk + it.hk;
-    x.bad = __any_sync(0xffffffffu, bad);
-    return x;
+// What a producer warp feeds a run's tiles from: box `lane` of a tile is hh slots
+// of one pool block. Block ids are read two tiles ahead and scales one, so no tile
+// waits for a look-up (with the look-ups in line, a tile took 1700 cycles before its
+// first copy went out, and the copies, not the arithmetic, bounded the kernels).
+constexpr int kNoBox = -0x7fffffff;  // the box holds no visible slot: not read
+
+template <int TS>
+__device__ __forceinline__ int feed_id(const PagedTcParams& p, const PagedItem& it, int tile) {
+    const int lane = threadIdx.x & 31, slot = tile * TS + lane * p.hh;
+    if (lane * p.hh >= TS || slot + p.hh <= it.lo || slot > it.last) return kNoBox;
+    return p.a.table[it.b * p.a.max_blocks + p.block_of(slot)];
 }
-// Their copies, `nb` column blocks of 128 bytes each, spread over the warp.
+__device__ __forceinline__ bool feed_bad(const PagedTcParams& p, int id) {
+    return id != kNoBox && (id < 0 || id >= p.a.num_blocks);
+}
+// Key and value scale of a box (of one that is not read: anything finite).
+__device__ __forceinline__ float2 feed_scales(const PagedTcParams& p, const PagedItem& it, int id) {
+    if (id < 0 || id >= p.a.num_blocks) return make_float2(1.f, 1.f);
+    const int64_t u = static_cast<int64_t>(id) * p.a.Hk + it.hk;
+    return make_float2(p.a.ks[u], p.a.vs[u]);
+}
+__device__ __forceinline__ void feed_store(StageScales* sc, float2 s) {
+    const int lane = threadIdx.x & 31;
+    if (lane < kMaxBoxes) sc->kv[lane] = make_float4(s.x, s.y, __log2f(s.y), __fdividef(1.f, s.y));
+}
+// The copies of a tile, `nb` column blocks of 128 bytes for each box (block 0 in
+// place of a bad id); with `expect`, lane 0 first announces them and `extra` more.
 template <int EB, int TS>
-__device__ __forceinline__ void paged_load_boxes(const PagedTcParams& p, const CUtensorMap* map,
-                                                 const PagedBoxes& x, uint32_t dst, int nb,
-                                                 uint32_t full, bool expect = true, int extra = 0) {
+__device__ __forceinline__ void feed_copy(const PagedTcParams& p, const PagedItem& it,
+                                          const CUtensorMap* map, int tile, int id, uint32_t dst,
+                                          int nb, uint32_t full, bool expect = true, int extra = 0) {
     constexpr int kElems = 128 / EB;  // elements of a column block
-    const int lane = threadIdx.x & 31, hh = p.hh, n = (x.pb - x.pa) * nb;
-    __syncwarp();  // the scales are written before lane 0's arrive publishes the tile
-    if (expect && lane == 0)
-        mbar_arrive_expect_tx(full, static_cast<uint32_t>((x.pb - x.pa) * (nb + extra) * hh * 128));
+    const int lane = threadIdx.x & 31;
+    const bool used = id != kNoBox;
+    // (the barrier among the lanes also orders their scales before the arrive)
+    const int n = __popc(__ballot_sync(0xffffffffu, used));
     __syncwarp();
-    for (int base = 0; base < n; base += 32) {
-        const int l = base + lane, c = x.pa + l / nb, k = l % nb;
-        const int z = __shfl_sync(0xffffffffu, x.z, c & 31), y = __shfl_sync(0xffffffffu, x.y, c & 31);
-        if (l < n)
-            tma_load_3d(dst + k * TS * 128 + static_cast<uint32_t>(c * hh * 128), map, kElems * k, y, z,
-                        full);
+    if (expect && lane == 0)
+        mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * (nb + extra) * p.hh * 128));
+    __syncwarp();
+    if (used) {
+        const int slot = tile * TS + lane * p.hh;
+        const int y = slot - p.block_of(slot) * p.a.bs;
+        const int z = (feed_bad(p, id) ? 0 : id) * p.a.Hk + it.hk;
+        const uint32_t to = dst + static_cast<uint32_t>(lane * p.hh * 128);
+        for (int k = 0; k < nb; ++k) tma_load_3d(to + k * TS * 128, map, kElems * k, y, z, full);
     }
+    __syncwarp();
 }
 
 // A query row for the 8-bit products, a warp at a time (lane: elements 4 lane ..

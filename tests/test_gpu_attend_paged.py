@@ -289,6 +289,23 @@ def test_strided_queries_streams_graphs_and_shared_workspace(pool):
         kvc.attention_over_paged_cache(**x, max_seqlen_q=1, workspace=ws[:need - 256])
 
 
+@pytest.mark.parametrize("dtype,pool,D", [("bf16", "e4m3", 128), ("f16", "f16", 64),
+                                          ("bf16", "bf16", 128), ("f16", "e5m2", 192)])
+def test_many_tiles_and_units_a_block(dtype, pool, D):
+    """Long runs: every ring, buffer and reference of a thread block is used many
+    times over, and units end inside a block's run; the timeout bit stays clear."""
+    lens = [(700, 5000), (1001, 1001), (330, 9000), (1, 4000)]
+    x = make(21, dtype, pool, lens, 16, 4, D, 128, 64)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = kvc.attention_over_paged_cache(**x, max_seqlen_q=1001, status=status)
+    assert int(status) == 0
+    check(x, got, 1001)
+    many = make(22, dtype, pool, [(1, 100 + 37 * i) for i in range(150)], 8, 8, D, 128, 64)
+    got = kvc.attention_over_paged_cache(**many, max_seqlen_q=1, status=status)
+    assert int(status) == 0
+    check(many, got, 1)
+
+
 def test_the_same_call_gives_the_same_bits():
     x = make(12, "bf16", "e4m3", [(1, 5000), (3, 700), (1, 12000)], 8, 2, 128, 128, 64)
     first = kvc.attention_over_paged_cache(**x, max_seqlen_q=3)
