@@ -242,7 +242,7 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
             mbar_drain(bars.full(q % p.ns), static_cast<uint32_t>((q / p.ns) & 1));
 }
 
-// One thread: S^T of every tile.
+// One warp: S^T of every tile.
 template <typename T, int EB, int DN>
 __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
                          uint32_t tmem) {
@@ -260,40 +260,51 @@ __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars,
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
-        if (!mbar_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
-        if (items[kb].flags & kItemDone) break;
-        const int nt = items[kb].nt;
+        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (uniform(items[kb].flags) & kItemDone) break;
+        const int nt = uniform(items[kb].nt);
         const uint32_t sQ = smem_addr(smem + p.off_q + kb * p.q_bytes);
         for (int n = 0; n < nt; ++n, ++c) {
             const int sb = c & 1;
-            if (!mbar_wait(bars.full(ring.s), ring.ph, abort) ||
-                (c >= 2 && !mbar_wait(bars.s_free(sb), static_cast<uint32_t>((c / 2 - 1) & 1), abort))) {
+            if (!warp_wait(bars.full(ring.s), ring.ph, abort) ||
+                (c >= 2 && !warp_wait(bars.s_free(sb), static_cast<uint32_t>((c / 2 - 1) & 1), abort))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const uint32_t sK = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes;
-            for (int part = 0; part < S::kParts; ++part)
-                for (int i = 0; i < ksteps; ++i) {
-                    const uint64_t da = smem_desc_sw128(sK + (i >> 2) * kTS * 128 + (i & 3) * 32, 16, 1024);
-                    const uint64_t db = smem_desc_sw128(
-                        sQ + (part * nkb + (i >> 2)) * S::nblk + (i & 3) * 32, 16, 1024);
-                    if (EB == 1)
-                        tc_mma_f8(tmem + sb * DN, da, db, idesc, (part | i) != 0);
-                    else
-                        tc_mma(tmem + sb * DN, da, db, idesc, i != 0);
+            if (elect_one()) {
+                for (int b = 0; b < nkb; ++b) {
+                    // column block b of both; 32 bytes of a row per instruction, 2 in
+                    // the descriptor's address field
+                    const uint64_t da = smem_desc_sw128(sK + b * kTS * 128, 16, 1024);
+#pragma unroll
+                    for (int part = 0; part < S::kParts; ++part) {
+                        const uint64_t db = smem_desc_sw128(sQ + (part * nkb + b) * S::nblk, 16, 1024);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (4 * b + i >= ksteps) break;
+                            if (EB == 1)
+                                tc_mma_f8(tmem + sb * DN, da + 2 * i, db + 2 * i, idesc, (b | part | i) != 0);
+                            else
+                                tc_mma(tmem + sb * DN, da + 2 * i, db + 2 * i, idesc, (b | i) != 0);
+                        }
+                    }
                 }
-            tc_commit(bars.s_ready(sb));
+                tc_commit(bars.s_ready(sb));
+            }
+            __syncwarp();
             ring.next(p.ns);
         }
-        if (ok) tc_commit(bars.item_empty(kb));  // once the products have read the query rows
+        if (ok && elect_one()) tc_commit(bars.item_empty(kb));  // once the products have read the query rows
     }
-    tc_commit(bars.drained());
+    if (elect_one()) tc_commit(bars.drained());
+    __syncwarp();
     volatile int never = 0;
-    mbar_wait(bars.drained(), 0u, &never);
+    warp_wait(bars.drained(), 0u, &never);
 }
 
-// One thread: O^T += V^T P^T of every tile; releases the stages.
+// One warp: O^T += V^T P^T of every tile; releases the stages.
 template <typename T, int EB, int DN>
 __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
                           uint32_t tmem) {
@@ -302,19 +313,21 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
     const uint32_t stage0 = smem_addr(smem + p.off_stage);
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
     const int nkb = (a.D * EB + 127) / 128;
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t idesc = EB == 1 ? mma_idesc_f8(128, DN, a.e5m2, true, true, false)
+                                   : mma_idesc_f16(128, DN, std::is_same<T, __nv_bfloat16>::value, false,
+                                                   true);
     Ring ring;
     int c = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
-        if (!mbar_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
-        if (items[kb].flags & kItemDone) break;
-        const int nt = items[kb].nt;
+        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (uniform(items[kb].flags) & kItemDone) break;
+        const int nt = uniform(items[kb].nt);
         for (int n = 0; n < nt; ++n, ++c) {
             const int pb = c % S::npt;
-            if (!mbar_wait(bars.full(ring.s), ring.ph, abort) ||
-                !mbar_wait(bars.p_ready(pb), static_cast<uint32_t>((c / S::npt) & 1), abort)) {
+            if (!warp_wait(bars.full(ring.s), ring.ph, abort) ||
+                !warp_wait(bars.p_ready(pb), static_cast<uint32_t>((c / S::npt) & 1), abort)) {
                 ok = false;
                 break;
             }
@@ -322,31 +335,36 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
             const uint32_t sV = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes +
                                 static_cast<uint32_t>(nkb * kTS * 128);
             const uint32_t sP = smem_addr(smem + p.off_p) + pb * S::pbytes;
-            if (EB == 1) {
+            if (elect_one()) {
+                const uint64_t da = smem_desc_sw128(sV, kTS * 128, 1024);
+                const uint64_t db = smem_desc_sw128(sP, 16, 1024);
+                const uint32_t tO = tmem + S::col_o;
+                if (EB == 1) {
 #pragma unroll
-                for (int part = 0; part < 3; ++part)
+                    for (int i = 0; i < 4; ++i)  // 32 slots per step
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)       // 32 slots per instruction
-                        tc_mma_f8(tmem + S::col_o, smem_desc_sw128(sV + i * 32 * 128, 16, 1024),
-                                  smem_desc_sw128(sP + part * S::nblk + i * 32, 16, 1024),
-                                  mma_idesc_f8(128, DN, a.e5m2, true, true, false),
-                                  n != 0 || (part | i) != 0);
-            } else {
+                        for (int part = 0; part < 3; ++part)
+                            tc_mma_f8(tO, da + i * (32 * 128 / 16), db + part * (S::nblk / 16) + 2 * i,
+                                      idesc, (n | part | i) != 0);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)           // 16 slots per instruction
-                    tc_mma(tmem + S::col_o, smem_desc_sw128(sV + i * 16 * 128, kTS * 128, 1024),
-                           smem_desc_sw128(sP + (i >> 2) * S::nblk + (i & 3) * 32, 16, 1024),
-                           mma_idesc_f16(128, DN, kBf16, false, true), (n | i) != 0);
+                    for (int i = 0; i < 8; ++i)  // 16 slots per step
+                        tc_mma(tO, da + i * (16 * 128 / 16), db + (i >> 2) * (S::nblk / 16) + 2 * (i & 3),
+                               idesc, (n | i) != 0);
+                }
+                tc_commit(bars.o_done(pb));
+                tc_commit(bars.empty(ring.s));
             }
-            tc_commit(bars.o_done(pb));
-            tc_commit(bars.empty(ring.s));
+            __syncwarp();
             ring.next(p.ns);
         }
-        if (ok) mbar_arrive(bars.item_empty(kb), 1u);
+        if (ok && elect_one()) mbar_arrive(bars.item_empty(kb), 1u);
+        __syncwarp();
     }
-    tc_commit(bars.drained());
+    if (elect_one()) tc_commit(bars.drained());
+    __syncwarp();
     volatile int never = 0;
-    mbar_wait(bars.drained(), 0u, &never);
+    warp_wait(bars.drained(), 0u, &never);
 }
 
 template <typename T, int EB, int NR, bool MOD>
@@ -670,15 +688,15 @@ __global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
     tc_fence_before();
     paged_plan<T, kTS, kThreads>(p, st);  // with block barriers
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemSlot);
+    const uint32_t tmem = uniform(*reinterpret_cast<volatile int*>(smem + kTmemSlot));
     launch_dependents();
 
     if (warp < 4) {
         softmax_warps<T, EB, NR, MOD>(p, smem, bars, abort, tmem, st);
     } else if (warp == kMmaWarp) {
-        if ((threadIdx.x & 31) == 0) s_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
+        s_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
     } else if (warp == kPvWarp) {
-        if ((threadIdx.x & 31) == 0) pv_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
+        pv_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
     } else if (warp == kProdWarp) {
         producer_warp<EB>(p, smem, bars, abort);
     } else {

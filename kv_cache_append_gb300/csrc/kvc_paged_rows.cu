@@ -217,7 +217,7 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
                        static_cast<uint32_t>((q / stages) & 1));
 }
 
-// One thread: S of every tile, into its group's buffer once the group's last
+// One warp: S of every tile, into its group's buffer once the group's last
 // P (in the same columns) has been read.
 template <typename T, int EB>
 __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
@@ -236,50 +236,54 @@ __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars,
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
-        if (!mbar_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
-        if (items[kb].flags & kItemDone) break;
-        const int nt = items[kb].nt;
+        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (uniform(items[kb].flags) & kItemDone) break;
+        const int nt = uniform(items[kb].nt);
         const uint32_t sQ = smem_addr(smem + p.off_q + kb * p.q_bytes);
         for (int n = 0; n < nt; ++n, ++c) {
             const int g = turn.g;
-            if (!mbar_wait(bars.k_full(kr.s), kr.ph, abort) ||
-                (c >= kGroups && !mbar_wait(bars.o_done(g), turn.ph ^ 1u, abort))) {
+            if (!warp_wait(bars.k_full(kr.s), kr.ph, abort) ||
+                (c >= kGroups && !warp_wait(bars.o_done(g), turn.ph ^ 1u, abort))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const uint32_t sK = sK0 + kr.s * nkb * kTS * 128;
             const uint32_t tS = tmem + kColS + 128 * g;
-            for (int b = 0; b < nkb; ++b) {
-                // column block b of both; 32 bytes of a row per instruction, 2 in the
-                // descriptor's address field
-                const uint64_t db = smem_desc_sw128(sK + b * kTS * 128, 16, 1024);
+            if (elect_one()) {
+                for (int b = 0; b < nkb; ++b) {
+                    // column block b of both; 32 bytes of a row per instruction, 2 in
+                    // the descriptor's address field
+                    const uint64_t db = smem_desc_sw128(sK + b * kTS * 128, 16, 1024);
 #pragma unroll
-                for (int part = 0; part < kParts; ++part) {
-                    const uint64_t da = smem_desc_sw128(sQ + (part * nkb + b) * kBlk, 16, 1024);
+                    for (int part = 0; part < kParts; ++part) {
+                        const uint64_t da = smem_desc_sw128(sQ + (part * nkb + b) * kBlk, 16, 1024);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (4 * b + i >= ksteps) break;
-                        if (EB == 1)
-                            tc_mma_f8(tS, da + 2 * i, db + 2 * i, idesc, (b | part | i) != 0);
-                        else
-                            tc_mma(tS, da + 2 * i, db + 2 * i, idesc, (b | i) != 0);
+                        for (int i = 0; i < 4; ++i) {
+                            if (4 * b + i >= ksteps) break;
+                            if (EB == 1)
+                                tc_mma_f8(tS, da + 2 * i, db + 2 * i, idesc, (b | part | i) != 0);
+                            else
+                                tc_mma(tS, da + 2 * i, db + 2 * i, idesc, (b | i) != 0);
+                        }
                     }
                 }
+                tc_commit(bars.s_ready(g));
+                tc_commit(bars.k_empty(kr.s));
             }
-            tc_commit(bars.s_ready(g));
-            tc_commit(bars.k_empty(kr.s));
+            __syncwarp();
             kr.next(p.ns);
             turn.next();
         }
-        if (ok) tc_commit(bars.item_empty(kb));  // once the products have read the query rows
+        if (ok && elect_one()) tc_commit(bars.item_empty(kb));  // once the products have read the query rows
     }
-    tc_commit(bars.drained());
+    if (elect_one()) tc_commit(bars.drained());
+    __syncwarp();
     volatile int never = 0;
-    mbar_wait(bars.drained(), 0u, &never);
+    warp_wait(bars.drained(), 0u, &never);
 }
 
-// One thread: O += P V of every tile.
+// One warp: O += P V of every tile.
 template <typename T, int EB>
 __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
                           uint32_t tmem) {
@@ -295,15 +299,15 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
-        if (!mbar_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
-        if (items[kb].flags & kItemDone) break;
-        const int nt = items[kb].nt;
+        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (uniform(items[kb].flags) & kItemDone) break;
+        const int nt = uniform(items[kb].nt);
         // the last run's O has been read
-        if (k > 0 && !mbar_wait(bars.o_free(), static_cast<uint32_t>((k - 1) & 1), abort)) break;
+        if (k > 0 && !warp_wait(bars.o_free(), static_cast<uint32_t>((k - 1) & 1), abort)) break;
         for (int n = 0; n < nt; ++n) {
             const int g = turn.g;
-            if (!mbar_wait(bars.v_full(vr.s), vr.ph, abort) ||
-                !mbar_wait(bars.p_ready(g), turn.ph, abort)) {
+            if (!warp_wait(bars.v_full(vr.s), vr.ph, abort) ||
+                !warp_wait(bars.p_ready(g), turn.ph, abort)) {
                 ok = false;
                 break;
             }
@@ -311,28 +315,33 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
             const uint32_t sV = sV0 + vr.s * nvb * kTS * 128;
             const uint32_t tP = tmem + kColS + 128 * g, tO = tmem + kColO;
             const uint64_t dv = smem_desc_sw128(sV, kTS * 128, 1024);
-            if (EB == 1) {
+            if (elect_one()) {
+                if (EB == 1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)  // 32 slots per step
+                    for (int i = 0; i < 4; ++i)  // 32 slots per step
 #pragma unroll
-                    for (int part = 0; part < 3; ++part)
-                        tc_mma_f8_ts(tO, tP + 24 * i + 8 * part,
-                                     dv + i * (32 * 128 / 16), idesc, (n | i | part) != 0);
-            } else {
+                        for (int part = 0; part < 3; ++part)
+                            tc_mma_f8_ts(tO, tP + 24 * i + 8 * part,
+                                         dv + i * (32 * 128 / 16), idesc, (n | i | part) != 0);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)  // 16 slots per step
-                    tc_mma_ts(tO, tP + 8 * i, dv + i * (16 * 128 / 16), idesc, (n | i) != 0);
+                    for (int i = 0; i < 8; ++i)  // 16 slots per step
+                        tc_mma_ts(tO, tP + 8 * i, dv + i * (16 * 128 / 16), idesc, (n | i) != 0);
+                }
+                tc_commit(bars.o_done(g));
+                tc_commit(bars.v_empty(vr.s));
             }
-            tc_commit(bars.o_done(g));
-            tc_commit(bars.v_empty(vr.s));
+            __syncwarp();
             vr.next(p.nv);
             turn.next();
         }
-        if (ok) mbar_arrive(bars.item_empty(kb), 1u);
+        if (ok && elect_one()) mbar_arrive(bars.item_empty(kb), 1u);
+        __syncwarp();
     }
-    tc_commit(bars.drained());
+    if (elect_one()) tc_commit(bars.drained());
+    __syncwarp();
     volatile int never = 0;
-    mbar_wait(bars.drained(), 0u, &never);
+    warp_wait(bars.drained(), 0u, &never);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -689,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     tc_fence_before();
     paged_plan<T, kTS, kThreads>(p, st);  // with block barriers
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemSlot);
+    const uint32_t tmem = uniform(*reinterpret_cast<volatile int*>(smem + kTmemSlot));
     launch_dependents();
 
     // 120 registers for a softmax thread, 56 for the others: 12 warps x 120 + 8 x 56 <=
@@ -700,9 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kSWarp) {
-            if ((threadIdx.x & 31) == 0) s_issuer<T, EB>(p, smem, bars, abort, tmem);
+            s_issuer<T, EB>(p, smem, bars, abort, tmem);
         } else if (warp == kPvWarp) {
-            if ((threadIdx.x & 31) == 0) pv_issuer<T, EB>(p, smem, bars, abort, tmem);
+            pv_issuer<T, EB>(p, smem, bars, abort, tmem);
         } else if (warp == kKWarp) {
             producer_warp<EB, true>(p, smem, bars, abort);
         } else if (warp == kVWarp) {

@@ -45,6 +45,21 @@ __device__ __forceinline__ uint32_t mma_idesc_f8(int M, int N, bool a_e5m2, bool
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// One lane of a converged warp. The issuing warps run as a whole, on values that
+// are the same in all lanes, and only the tensor-core instructions stand behind
+// this: their operands are then uniform registers. (Issued by a lone thread of a
+// diverged warp, an instruction took 130 to 270 cycles, and the issue, not the products,
+// bounded the kernels.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+// A value that all lanes hold, as one the compiler knows to be uniform.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
 // The slots that query rows [r0, r0 + RG) of a sequence see, and their tiles.
 struct PagedGroup {
     int first, last;  // positions of the group's first and last row
