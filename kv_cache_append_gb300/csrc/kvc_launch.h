@@ -175,6 +175,7 @@ struct AppendParams {
     float* value_scale;
     void* out_query;
     int32_t* status;
+    int threads;          // of a block
     int tpb;              // tokens per block of the first tok_blocks blocks
     unsigned tok_blocks;
     int64_t seq_blocks;   // 8-bit pools: pool blocks a sequence can touch

@@ -2,6 +2,7 @@
 // (include/kvc.h): argument checks and launch plans. Nothing here allocates or
 // synchronises.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -54,11 +55,16 @@ int64_t span(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t w, int64_t 
 }
 
 bool current_is_gb300() {
+    static std::atomic<uint64_t> known{0};  // devices found to be sm_103
     int dev = 0, major = 0, minor = 0;
-    return cudaGetDevice(&dev) == cudaSuccess &&
-           cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
-           cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
-           major == 10 && minor == 3;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+    if (dev < 64 && (known.load(std::memory_order_relaxed) >> dev & 1u)) return true;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        major != 10 || minor != 3)
+        return false;
+    if (dev < 64) known.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return true;
 }
 
 // The CUDA-core kernel's splits of the slots: enough blocks for every SM to
@@ -296,7 +302,11 @@ int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int6
     p.tpb = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxTokensPerBlock,
                                                                     T / (8 * kPlanSms))));
     p.tok_blocks = static_cast<unsigned>((T + p.tpb - 1) / p.tpb);
+    p.threads = 256;
     if (eight(d)) {
+        // a block's second pass takes up to two jobs of a thread out of registers
+        const int64_t row_jobs = std::max((d.D - half) / ve, d.Dv / ve);
+        if (row_jobs <= 128 && std::min(d.max_q, d.block_size) * row_jobs <= 256) p.threads = 128;
         p.seq_blocks = std::min<int64_t>((d.max_q + d.block_size - 2) / d.block_size + 1, d.max_blocks);
         p.units8 = d.B * p.seq_blocks * d.Hk * 2;
     }

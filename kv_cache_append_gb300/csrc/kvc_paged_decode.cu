@@ -152,35 +152,7 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
             rd->lim[lane] = live ? it.K - it.S + r / a.G : -1;
             rd->slope[lane] = live && a.slopes ? a.slopes[it.hk * a.G + r % a.G] * kLog2e : 0.f;
         }
-#pragma unroll 2
-        for (int r = 0; r < DN; ++r) {
-            const int rr = it.r0 + r;
-            const bool live = r < p.RG && rr < R;
-            const T* q = static_cast<const T*>(a.q) + (it.q0 + (live ? rr / a.G : 0)) * a.q_tok +
-                         (static_cast<int64_t>(it.hk) * a.G + (live ? rr % a.G : 0)) * a.q_head;
-            if (EB == 2) {
-                for (int c = lane; c < nkb * 8; c += 32) {  // 16-byte chunks
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (live && c * 8 < a.D) v = *reinterpret_cast<const uint4*>(q + c * 8);
-                    *reinterpret_cast<uint4*>(sq + (c >> 3) * S::nblk + r * 128 +
-                                              (((c & 7) ^ (r & 7)) << 4)) = v;
-                }
-                if (lane == 0) rd->mul[r] = a.scale;
-            } else {
-                float x[2][4];
-                const float f = load_row_part<T>(q, a.D, live, lane, x);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (c >= nkb) break;
-                    uint32_t hi, lo;
-                    split_row_part(x[c], f, hi, lo);
-                    const int o = c * S::nblk + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t*>(sq + o) = hi;
-                    *reinterpret_cast<uint32_t*>(sq + nkb * S::nblk + o) = lo;
-                }
-                if (lane == 0) rd->mul[r] = a.scale * (1.f / f);  // f is a power of two
-            }
-        }
+        prepare_rows<T, EB, DN>(p, it, sq, nkb, S::nblk, 0, 1, lane, rd->mul);
         fence_async_shared();  // the query rows, for the tensor cores
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);
@@ -711,73 +683,94 @@ __global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
     if (threadIdx.x == 0 && *abort && p.a.status) atomicOr(p.a.status, KVC_DEV_TIMEOUT);
 }
 
-// Block (c, y): the unit whose second block is c, rows y, y + gridDim.y, ...
-// 8 warps take the partials in turn, a lane four value columns.
-template <typename T>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedTcParams p) {
-    __shared__ float sh[8][128];
-    __shared__ float shl[8];
+// Block (c, y): the unit whose second block is c, 8 / WPR of its rows. WPR warps
+// take a row's partials in turn, a lane four value columns, eight loads under way.
+constexpr int kMergeWarps = 8;
+template <typename T, int WPR>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedTcParams p) {
+    __shared__ float4 sh[kMergeWarps][32];
+    __shared__ float shl[kMergeWarps];
     grid_dependency_wait();
     const PagedAttendParams& a = p.a;
     const PagedRec rec = p.rec[blockIdx.x];
     if (!rec.valid || static_cast<int>(blockIdx.x) != rec.c0 + 1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y * (kMergeWarps / WPR) + warp / WPR, part = warp % WPR;
     const int n = rec.c1 - rec.c0 + 1;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
     auto slot = [&](int k) -> int64_t {
-        return 2 * static_cast<int64_t>(rec.c0 + k) + (k == 0 ? 1 : 0);
+        return (2 * static_cast<int64_t>(rec.c0 + k) + (k == 0 ? 1 : 0)) * p.RG + r;
     };
-    for (int r = blockIdx.y; r < rec.rows; r += gridDim.y) {
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    int bad = 0;
+    if (r < rec.rows) {
         float m = -INFINITY;
-        int bad = 0;
         for (int k = lane; k < n; k += 32) {
-            const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[slot(k) * p.RG + r];
-            if (ml.y < 0.f) bad = 1;
-            if (ml.y != 0.f) m = fmaxf(m, ml.x);
+            const float2 x = ml[slot(k)];
+            if (x.y < 0.f) bad = 1;
+            if (x.y != 0.f) m = fmaxf(m, x.x);
         }
 #pragma unroll
         for (int o = 16; o >= 1; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         bad = __any_sync(0xffffffffu, bad);
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = warp; k < n; k += 8) {
-            const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[slot(k) * p.RG + r];
-            const float f = ml.y == 0.f ? 0.f : ml.x == m ? 1.f : fast_exp2(ml.x - m);
-            const float* src = p.part_acc + (slot(k) * p.RG + r) * a.Dv + 4 * lane;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (4 * lane < a.Dv) v = *reinterpret_cast<const float4*>(src);
-            if (ml.y != 0.f) {
-                l = fmaf(ml.y, f, l);
-                acc.x = fmaf(v.x, f, acc.x);
-                acc.y = fmaf(v.y, f, acc.y);
-                acc.z = fmaf(v.z, f, acc.z);
-                acc.w = fmaf(v.w, f, acc.w);
+        constexpr int kAhead = 8;
+        for (int k0 = part; k0 < n; k0 += kAhead * WPR) {
+            float4 v[kAhead];
+            float2 x[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int k = k0 + i * WPR;
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                x[i] = make_float2(0.f, 0.f);
+                if (k < n) {
+                    x[i] = ml[slot(k)];
+                    if (4 * lane < a.Dv)
+                        v[i] = *reinterpret_cast<const float4*>(p.part_acc + slot(k) * a.Dv + 4 * lane);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (x[i].y == 0.f) continue;
+                const float f = x[i].x == m ? 1.f : fast_exp2(x[i].x - m);
+                l = fmaf(x[i].y, f, l);
+                acc.x = fmaf(v[i].x, f, acc.x);
+                acc.y = fmaf(v[i].y, f, acc.y);
+                acc.z = fmaf(v[i].z, f, acc.z);
+                acc.w = fmaf(v[i].w, f, acc.w);
             }
         }
-        reinterpret_cast<float4*>(sh[warp])[lane] = acc;
+    }
+    if (WPR > 1) {
+        sh[warp][lane] = acc;
         if (lane == 0) shl[warp] = l;
         __syncthreads();
-        if (threadIdx.x < a.Dv) {
-            float o = 0.f, ll = 0.f;
+        if (part != 0) return;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                o += sh[w][threadIdx.x];
-                ll += shl[w];
-            }
-            const int rr = rec.r0 + r;
-            const int64_t row = static_cast<int64_t>(rec.q0 + rr / a.G) * a.Hq + rec.hk * a.G + rr % a.G;
-            static_cast<T*>(a.out)[row * a.Dv + threadIdx.x] =
-                Storage<T>::from_float(bad ? 0.f : __fdiv_rn(o, ll));
+        for (int w = 1; w < WPR; ++w) {
+            const float4 v = sh[warp + w][lane];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+            l += shl[warp + w];
         }
-        __syncthreads();
+    }
+    if (r < rec.rows && 4 * lane < a.Dv) {
+        const int rr = rec.r0 + r;
+        const int64_t row = static_cast<int64_t>(rec.q0 + rr / a.G) * a.Hq + rec.hk * a.G + rr % a.G;
+        T* o = static_cast<T*>(a.out) + row * a.Dv + 4 * lane;
+        const float x[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = Storage<T>::from_float(bad ? 0.f : __fdiv_rn(x[e], l));
     }
 }
 
 template <typename T, int EB, int NR, bool MOD>
 cudaError_t launch_t(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
     auto kern = paged_decode_kernel<T, EB, NR, MOD>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern));
     if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(p.ctas), kThreads, smem, stream>>>(p);
     return cudaGetLastError();
@@ -804,19 +797,28 @@ cudaError_t launch_paged_decode(const PagedTcParams& p, int dtype, int pool_dtyp
                              : launch_eb<__half, 1>(p, nr, smem, stream);
 }
 
-cudaError_t launch_paged_merge(const PagedTcParams& p, int dtype, cudaStream_t stream) {
-    if (p.ctas < 2) return cudaSuccess;
+template <typename T>
+static cudaError_t launch_merge_t(const PagedTcParams& p, cudaStream_t stream) {
+    // few rows: more warps for each (a long context's unit can have hundreds of partials)
+    const int wpr = p.RG <= 16 ? 4 : p.RG <= 32 ? 2 : 1, per = kMergeWarps / wpr;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(std::min(p.RG, 8)));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>((p.RG + per - 1) / per));
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return dtype == KVC_BF16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, p)
-                             : cudaLaunchKernelEx(&cfg, paged_merge_kernel<__half>, p);
+    return wpr == 4   ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 4>, p)
+           : wpr == 2 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 2>, p)
+                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 1>, p);
+}
+
+cudaError_t launch_paged_merge(const PagedTcParams& p, int dtype, cudaStream_t stream) {
+    if (p.ctas < 2) return cudaSuccess;
+    return dtype == KVC_BF16 ? launch_merge_t<__nv_bfloat16>(p, stream)
+                             : launch_merge_t<__half>(p, stream);
 }
 
 }  // namespace kvc

@@ -119,40 +119,11 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
         }
         unsigned char* sq = smem + p.off_q + kb * p.q_bytes;
         float* mul = reinterpret_cast<float*>(sq + 2 * nkb * kBlk);  // 8-bit pools
-        const int R = it.S * a.G;
         if (qw == 0 && lane == 0) {
             items[kb] = it;
             *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 0;
         }
-#pragma unroll 2
-        for (int r = qw; r < kRows; r += 4) {
-            const int rr = it.r0 + r;
-            const bool live = rr < R;
-            const T* q = static_cast<const T*>(a.q) +
-                         static_cast<int64_t>(it.q0 + (live ? rr / a.G : 0)) * a.q_tok +
-                         (static_cast<int64_t>(it.hk) * a.G + (live ? rr % a.G : 0)) * a.q_head;
-            if (EB == 2) {
-                for (int c = lane; c < nkb * 8; c += 32) {  // 16-byte chunks
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (live && c * 8 < a.D) v = *reinterpret_cast<const uint4*>(q + c * 8);
-                    *reinterpret_cast<uint4*>(sq + (c >> 3) * kBlk + r * 128 +
-                                              (((c & 7) ^ (r & 7)) << 4)) = v;
-                }
-            } else {
-                float x[2][4];
-                const float f = load_row_part<T>(q, a.D, live, lane, x);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (c >= nkb) break;
-                    uint32_t hi, lo;
-                    split_row_part(x[c], f, hi, lo);
-                    const int o = c * kBlk + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t*>(sq + o) = hi;
-                    *reinterpret_cast<uint32_t*>(sq + nkb * kBlk + o) = lo;
-                }
-                if (lane == 0) mul[r] = a.scale * (1.f / f);  // f is a power of two
-            }
-        }
+        prepare_rows<T, EB, kRows>(p, it, sq, nkb, kBlk, qw, 4, lane, EB == 1 ? mul : nullptr);
         fence_async_shared();  // the query rows, for the tensor cores
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);
@@ -732,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
 template <typename T, int EB, bool MOD>
 cudaError_t launch_t(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
     auto kern = paged_rows_kernel<T, EB, MOD>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern));
     if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(p.ctas), kThreads, smem, stream>>>(p);
     return cudaGetLastError();

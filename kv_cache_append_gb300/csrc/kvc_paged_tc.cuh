@@ -16,6 +16,7 @@
 
 #include <cuda.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "kvc_launch.h"
@@ -24,6 +25,20 @@
 #include "kvc_tcgen05.cuh"
 
 namespace kvc {
+
+// A kernel's dynamic shared memory limit, raised to the block's most once per device.
+struct SmemLimit {
+    std::atomic<uint64_t> done{0};
+    cudaError_t raise(const void* kern) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1u)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4: 8-bit operands (each of its
 // own format), fp32 accumulate, 32 elements of K per instruction.
@@ -308,63 +323,122 @@ __device__ __forceinline__ void feed_copy(const PagedTcParams& p, const PagedIte
     constexpr int kElems = 128 / EB;  // elements of a column block
     const int lane = threadIdx.x & 31;
     const bool used = id != kNoBox;
-    // (the barrier among the lanes also orders their scales before the arrive)
-    const int n = __popc(__ballot_sync(0xffffffffu, used));
+    // the boxes in use follow one another (and the vote orders the lanes' scales
+    // before the arrive that publishes the tile)
+    const uint32_t mask = __ballot_sync(0xffffffffu, used);
+    const int first = __ffs(mask) - 1, n = __popc(mask);
+    const int slot = tile * TS + lane * p.hh;
+    const int y = used ? slot - p.block_of(slot) * p.a.bs : 0;
+    const int z = used ? (feed_bad(p, id) ? 0 : id) * p.a.Hk + it.hk : 0;
     __syncwarp();
-    if (expect && lane == 0)
+    if (expect && elect_one())
         mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * (nb + extra) * p.hh * 128));
     __syncwarp();
-    if (used) {
-        const int slot = tile * TS + lane * p.hh;
-        const int y = slot - p.block_of(slot) * p.a.bs;
-        const int z = (feed_bad(p, id) ? 0 : id) * p.a.Hk + it.hk;
-        const uint32_t to = dst + static_cast<uint32_t>(lane * p.hh * 128);
-        for (int k = 0; k < nb; ++k) tma_load_3d(to + k * TS * 128, map, kElems * k, y, z, full);
+    for (int c = first; c < first + n; ++c) {
+        const int yc = uniform(lane == c ? y : 0), zc = uniform(lane == c ? z : 0);
+        const uint32_t to = dst + static_cast<uint32_t>(c * p.hh * 128);
+        if (elect_one())
+            for (int k = 0; k < nb; ++k) tma_load_3d(to + k * TS * 128, map, kElems * k, yc, zc, full);
+        __syncwarp();
     }
-    __syncwarp();
 }
 
-// A query row for the 8-bit products, a warp at a time (lane: elements 4 lane ..
-// of each 128): its elements, and the power of two that takes the largest into
-// [2^7, 2^8).
-template <typename T>
-__device__ __forceinline__ float load_row_part(const T* q, int D, bool live, int lane, float (&x)[2][4]) {
-    float big = 0.f;
+// A run's query rows into the swizzled operand layout, by one warp: rows w0, w0 +
+// step, ... of ROWS (rows past the unit's are zero). 8-bit products: hi parts, then
+// lo parts, both e4m3, of the row times the power of two that takes its largest
+// element into [2^7, 2^8); mul[r] is the score scale over that power. Several rows'
+// loads are under way at a time: one by one, the 32 rows of a warp took 20 us.
+template <typename T, int EB, int ROWS>
+__device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const PagedItem& it,
+                                             unsigned char* sq, int nkb, int blk, int w0, int step,
+                                             int lane, float* mul) {
+    const PagedAttendParams& a = p.a;
+    const int R = min(p.RG, it.S * a.G - it.r0);
+    const T* base = static_cast<const T*>(a.q) + static_cast<int64_t>(it.hk) * a.G * a.q_head;
+    auto row_ptr = [&](int r) {
+        const int rr = it.r0 + r, t = rr / a.G;
+        return base + (it.q0 + t) * a.q_tok + (rr - t * a.G) * a.q_head;
+    };
+    if (EB == 2) {
+        // 16-byte chunks of the rows in one list
+        const int cpr = nkb * 8, n = ROWS / step * cpr;
+        constexpr int kAhead = 4;
+        for (int i0 = lane; i0 < n; i0 += 32 * kAhead) {
+            uint4 v[kAhead];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int d = c * 128 + lane * 4;
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + 32 * u, r = w0 + i / cpr * step, c = i % cpr;
+                v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (i < n && r < R && c * 8 < a.D)
+                    v[u] = *reinterpret_cast<const uint4*>(row_ptr(r) + c * 8);
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
-        if (live && d < D) {
-            const uint2 v = *reinterpret_cast<const uint2*>(q + d);
-            const T* h = reinterpret_cast<const T*>(&v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[c][e] = Storage<T>::to_float(h[e]);
-                if (fabsf(x[c][e]) < INFINITY)
-                    big = fmaxf(big, fabsf(x[c][e]));
-                else
-                    x[c][e] = __uint_as_float(0x7fffffffu);  // no 8-bit infinity: NaN
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + 32 * u, r = w0 + i / cpr * step, c = i % cpr;
+                if (i < n)
+                    *reinterpret_cast<uint4*>(sq + (c >> 3) * blk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                        v[u];
             }
         }
+        if (mul)
+            for (int r = w0 + lane * step; r < ROWS; r += 32 * step) mul[r] = a.scale;
+        return;
     }
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    int e2 = 7 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
-    e2 = max(-120, min(120, e2));
-    return __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
-}
-// Four of its elements, scaled, as hi + lo, both e4m3.
-__device__ __forceinline__ void split_row_part(const float (&x)[4], float f, uint32_t& hi, uint32_t& lo) {
-    hi = lo = 0;
+    constexpr int kAhead = 4;  // rows
+    for (int r0 = w0; r0 < ROWS; r0 += kAhead * step) {
+        uint2 v[kAhead][2];  // lane: elements 4 lane .. of each 128
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-        const float u = x[e] * f, v = x[e + 1] * f;
-        const uint32_t h2 = to_eight2<false>(u, v);
-        const float2 hf = from_eight2<false>(h2);
-        hi |= h2 << (8 * e);
-        lo |= to_eight2<false>(u - hf.x, v - hf.y) << (8 * e);
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = r0 + u * step;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int d = c * 128 + lane * 4;
+                v[u][c] = make_uint2(0u, 0u);
+                if (r < R && d < a.D) v[u][c] = *reinterpret_cast<const uint2*>(row_ptr(r) + d);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = r0 + u * step;
+            if (r >= ROWS) break;
+            float x[2][4], big = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const T* h = reinterpret_cast<const T*>(&v[u][c]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[c][e] = Storage<T>::to_float(h[e]);
+                    if (fabsf(x[c][e]) < INFINITY)
+                        big = fmaxf(big, fabsf(x[c][e]));
+                    else
+                        x[c][e] = __uint_as_float(0x7fffffffu);  // no 8-bit infinity: NaN
+                }
+            }
+            big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+            int e2 = 7 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
+            e2 = max(-120, min(120, e2));
+            const float f = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (c >= nkb) break;
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float y0 = x[c][e] * f, y1 = x[c][e + 1] * f;
+                    const uint32_t h2 = to_eight2<false>(y0, y1);
+                    const float2 hf = from_eight2<false>(h2);
+                    hi |= h2 << (8 * e);
+                    lo |= to_eight2<false>(y0 - hf.x, y1 - hf.y) << (8 * e);
+                }
+                const int o = c * blk + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+                *reinterpret_cast<uint32_t*>(sq + o) = hi;
+                *reinterpret_cast<uint32_t*>(sq + nkb * blk + o) = lo;
+            }
+            if (lane == 0) mul[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+        }
     }
 }
+
 // Four weights as three e5m2 parts each (a word of four codes per part). e5m2
 // is the upper byte of fp16, so from the weights in fp16 the first two parts are
 // cut off by a mask, each difference is exact, and the last is rounded: 3 + 3 + 3

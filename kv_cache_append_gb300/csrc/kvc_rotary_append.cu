@@ -13,8 +13,8 @@
 // inputs' type, write the keys and values, each a pure stream: every byte is
 // read and written once); with an 8-bit pool the remaining blocks each take one
 // (sequence, touched pool block, head, keys or values): a pass over the block's
-// new rows for the largest absolute value, the block's scale, a second pass
-// (out of L1) that rounds and stores.
+// new rows for the largest absolute value, the block's scale, and a second pass,
+// out of registers, that rounds and stores.
 //
 // 8-bit pools: the scale is 2^e, e the least with amax <= 1.75 * 2^top * 2^e,
 // never below the scale of rows that the block already holds; a power of two
@@ -144,105 +144,139 @@ __device__ __forceinline__ void row_job(const AppendParams& p, const T* src, int
     }
 }
 
-// The sequence is within the contract, the block ids of its new slots
-// included (all threads of the block take part; the answer is the same for all).
-__device__ __forceinline__ bool append_ok(const AppendParams& p, int64_t b, const PagedSeq& s) {
-    int bad = !s.ok || (s.S > 0 && s.K > p.num_pos);
-    if (!bad && s.S > 0) {
+// The sequence is within the contract, its block ids aside.
+__device__ __forceinline__ bool append_ok(const AppendParams& p, const PagedSeq& s) {
+    return s.ok && (s.S == 0 || s.K <= p.num_pos);
+}
+// A block id of its new slots lies outside the pool (all threads of the block take
+// part; the answer is the same for all).
+__device__ __forceinline__ bool append_bad_ids(const AppendParams& p, int64_t b, const PagedSeq& s) {
+    int bad = 0;
+    if (s.S > 0) {
         const int i0 = (s.K - s.S) / p.bs, i1 = (s.K - 1) / p.bs;
         for (int i = i0 + threadIdx.x; i <= i1; i += blockDim.x) {
             const int id = p.table[b * p.max_blocks + i];
             bad |= id < 0 || id >= p.num_blocks;
         }
     }
-    return !__syncthreads_or(bad);
+    return __syncthreads_or(bad);
+}
+
+// Rows of `heads` heads for each of the block's tokens: a thread keeps one job of
+// a row and steps over the rows, so that nothing is divided in the loop.
+template <typename T, int VE, typename Dst>
+__device__ __forceinline__ void token_rows(const AppendParams& p, const T* src, int64_t tok0, int nt,
+                                           int heads, int jobs, int64_t st_tok, int64_t st_head,
+                                           bool rotate, const int* pos, bool zero_bad, Dst dst_of) {
+    const int step = blockDim.x / jobs;
+    int h = threadIdx.x / jobs;
+    if (h >= step) return;
+    const int j = threadIdx.x - h * jobs;
+    int i = 0;
+    for (;;) {
+        while (h >= heads) {
+            h -= heads;
+            ++i;
+        }
+        if (i >= nt) return;
+        const int at = pos[i];  // -1: outside the contract, -2: of no sequence
+        if (at >= 0 || (at == -1 && zero_bad)) {
+            const int64_t a = static_cast<int64_t>(max(at, 0)) * p.half;
+            float y[2 * VE];
+            int o0, o1;
+            row_job<T, VE, false>(p, src + (tok0 + i) * st_tok + h * st_head, j, rotate, p.cos + a,
+                                  p.sin + a, y, o0, o1);
+            if (at < 0) {
+#pragma unroll
+                for (int e = 0; e < 2 * VE; ++e) y[e] = 0.f;
+            }
+            T* dst = dst_of(i, h);
+            store_vec<T, VE>(dst + o0, y);
+            if (o1 >= 0) store_vec<T, VE>(dst + o1, y + VE);
+        }
+        h += step;
+    }
 }
 
 // Blocks [0, p.tok_blocks): p.tpb tokens each.
 template <typename T, bool EIGHT, int VE>
 __device__ void append_tokens(const AppendParams& p) {
-    __shared__ int64_t dst_row[kMaxTokensPerBlock];  // pool row (of head 0) of the token's slot; -1: none
+    __shared__ int64_t dst_row[kMaxTokensPerBlock];  // pool row (of head 0) of the token's slot
     __shared__ int pos[kMaxTokensPerBlock];          // position; -1: outside the contract, -2: no sequence
+    __shared__ int seq[kMaxTokensPerBlock];
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tpb;
     const int nt = static_cast<int>(min(static_cast<int64_t>(p.tpb), p.total_q - tok0));
+    if (static_cast<int>(threadIdx.x) < nt) {
+        // the first sequence whose end lies past the token
+        const int tok = static_cast<int>(tok0) + threadIdx.x;
+        int lo = 0, hi = static_cast<int>(p.B);
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.cu[mid + 1] <= tok) lo = mid + 1; else hi = mid;
+        }
+        seq[threadIdx.x] = lo;
+    }
+    __syncthreads();
+    PagedSeq s{};
+    bool ok = false;
     for (int i = 0; i < nt; ++i) {
-        const int tok = static_cast<int>(tok0) + i;
-        // the sequence: how many of the ends cu[1..B] lie at or before the token
-        int64_t b = 0;
-        for (int64_t c = 0; c < p.B; c += blockDim.x) {
-            const int64_t e = c + threadIdx.x;
-            b += __syncthreads_count(e < p.B && p.cu[e + 1] <= tok);
+        const int b = seq[i];
+        if (i == 0 || b != seq[i - 1]) {
+            if (b < p.B) s = paged_seq(p.cu, p.kl, b, p.total_q, p.max_q, p.M);
+            ok = b < p.B && append_ok(p, s) && !append_bad_ids(p, b, s);
         }
-        PagedSeq s{};
-        bool mine = b < p.B;
-        if (mine) {
-            s = paged_seq(p.cu, p.kl, b, p.total_q, p.max_q, p.M);
-            mine = s.rows_ok && tok >= s.q0 && tok < s.q0 + s.S;
-        }
-        const bool ok = mine && append_ok(p, b, s);
-        if (threadIdx.x == 0) {
-            const int j = s.K - s.S + (tok - s.q0);
-            pos[i] = ok ? j : (mine ? -1 : -2);
-            dst_row[i] = -1;
-            if (ok)
-                dst_row[i] = (static_cast<int64_t>(p.table[b * p.max_blocks + j / p.bs]) * p.Hk) *
-                                 p.bs + j % p.bs;
+        if (static_cast<int>(threadIdx.x) == i) {
+            const int t = static_cast<int>(tok0) + i - s.q0;
+            const bool mine = b < p.B && s.rows_ok && t >= 0 && t < s.S;
+            const int j = s.K - s.S + t;
+            pos[i] = !mine ? -2 : ok ? j : -1;
+            if (mine && ok)
+                dst_row[i] = (static_cast<int64_t>(p.table[b * p.max_blocks + j / p.bs]) * p.Hk) * p.bs +
+                             j % p.bs;
             else if (mine && p.status)
                 atomicOr(p.status, KVC_DEV_OVERFLOW);
         }
     }
     __syncthreads();
     const int jr = (p.half + (p.D - 2 * p.half)) / VE, jv = p.Dv / VE;
-    const int nq = p.Hq * jr, nk = EIGHT ? 0 : p.Hk * jr, nv = EIGHT ? 0 : p.Hk * jv;
-    const int per = nq + nk + nv;
-    for (int i = 0; i < nt; ++i) {
-        const int j = pos[i];
-        if (j == -2) continue;  // behind the last sequence: left as it was
-        const int64_t tok = tok0 + i;
-        const float* cosr = p.cos + static_cast<int64_t>(max(j, 0)) * p.half;
-        const float* sinr = p.sin + static_cast<int64_t>(max(j, 0)) * p.half;
-        for (int w = threadIdx.x; w < per; w += blockDim.x) {
-            float y[2 * VE];
-            int o0, o1;
-            T* dst;
-            if (w < nq) {
-                const int h = w / jr;
-                dst = static_cast<T*>(p.out_query) + (tok * p.Hq + h) * p.D;
-                row_job<T, VE, false>(p, static_cast<const T*>(p.query) + tok * p.st[0] + h * p.st[1],
-                                      w - h * jr, true, cosr, sinr, y, o0, o1);
-                if (j < 0) {
-#pragma unroll
-                    for (int e = 0; e < 2 * VE; ++e) y[e] = 0.f;
-                }
-            } else {
-                if (j < 0) break;
-                const bool key = w < nq + nk;
-                const int v = key ? w - nq : w - nq - nk, jn = key ? jr : jv;
-                const int h = v / jn;
-                const int64_t r = dst_row[i] + static_cast<int64_t>(h) * p.bs;
-                dst = static_cast<T*>(key ? p.key_pool : p.value_pool) + r * (key ? p.D : p.Dv);
-                const T* src = key ? static_cast<const T*>(p.new_key) + tok * p.st[2] + h * p.st[3]
-                                   : static_cast<const T*>(p.new_value) + tok * p.st[4] + h * p.st[5];
-                row_job<T, VE, false>(p, src, v - h * jn, key, cosr, sinr, y, o0, o1);
-            }
-            store_vec<T, VE>(dst + o0, y);
-            if (o1 >= 0) store_vec<T, VE>(dst + o1, y + VE);
-        }
-    }
+    token_rows<T, VE>(p, static_cast<const T*>(p.query), tok0, nt, p.Hq, jr, p.st[0], p.st[1], true,
+                      pos, true, [&](int i, int h) {
+                          return static_cast<T*>(p.out_query) + ((tok0 + i) * p.Hq + h) * p.D;
+                      });
+    if (EIGHT) return;
+    token_rows<T, VE>(p, static_cast<const T*>(p.new_key), tok0, nt, p.Hk, jr, p.st[2], p.st[3], true,
+                      pos, false, [&](int i, int h) {
+                          return static_cast<T*>(p.key_pool) +
+                                 (dst_row[i] + static_cast<int64_t>(h) * p.bs) * p.D;
+                      });
+    token_rows<T, VE>(p, static_cast<const T*>(p.new_value), tok0, nt, p.Hk, jv, p.st[4], p.st[5],
+                      false, pos, false, [&](int i, int h) {
+                          return static_cast<T*>(p.value_pool) +
+                                 (dst_row[i] + static_cast<int64_t>(h) * p.bs) * p.Dv;
+                      });
 }
 
 // One (sequence, touched block, head, keys or values) of an 8-bit pool.
 template <typename T, bool E5M2, int VE>
-__device__ void append_block8(const AppendParams& p, int64_t idx) {
+__device__ void append_block8(const AppendParams& p, int64_t unit_index) {
     __shared__ uint32_t red[kAppThreads / 32];
-    const int which = static_cast<int>(idx & 1);  // 0: keys, 1: values
-    idx >>= 1;
-    const int hk = static_cast<int>(idx % p.Hk);
-    idx /= p.Hk;
-    const int64_t b = idx / p.seq_blocks;
-    const int ib = static_cast<int>(idx - b * p.seq_blocks);
+    const int which = static_cast<int>(unit_index & 1);  // 0: keys, 1: values
+    int hk, ib;
+    int64_t b;
+    if (p.units8 < (int64_t(1) << 31)) {
+        const uint32_t i = static_cast<uint32_t>(unit_index) >> 1, j = i / p.Hk;
+        hk = static_cast<int>(i - j * p.Hk);
+        const uint32_t q = j / static_cast<uint32_t>(p.seq_blocks);
+        ib = static_cast<int>(j - q * static_cast<uint32_t>(p.seq_blocks));
+        b = q;
+    } else {
+        const int64_t i = unit_index >> 1, j = i / p.Hk;
+        hk = static_cast<int>(i - j * p.Hk);
+        b = j / p.seq_blocks;
+        ib = static_cast<int>(j - b * p.seq_blocks);
+    }
     const PagedSeq s = paged_seq(p.cu, p.kl, b, p.total_q, p.max_q, p.M);
-    if (!append_ok(p, b, s)) {
+    if (!append_ok(p, s)) {
         if (threadIdx.x == 0 && ib == 0 && p.status) atomicOr(p.status, KVC_DEV_OVERFLOW);
         return;
     }
@@ -250,40 +284,60 @@ __device__ void append_block8(const AppendParams& p, int64_t idx) {
     const int start = s.K - s.S;
     const int i = start / p.bs + ib;
     const int lo = max(start, i * p.bs), hi = min(s.K, (i + 1) * p.bs);
-    if (lo >= hi) return;
-    const int64_t blk = p.table[b * p.max_blocks + i];
-    const int64_t unit = blk * p.Hk + hk;
-    float* sp = (which ? p.value_scale : p.key_scale) + unit;
-    const int held = lo - i * p.bs;  // rows that the block already holds
-    const float old = held ? *sp : 0.f;
     const int width = which ? p.Dv : p.D;
     const int jn = which ? p.Dv / VE : (p.half + (p.D - 2 * p.half)) / VE;
-    const T* src0 = static_cast<const T*>(which ? p.new_value : p.new_key) + hk * p.st[which ? 5 : 3];
+    const T* src0 = static_cast<const T*>(which ? p.new_value : p.new_key) + hk * p.st[which ? 5 : 3] +
+                    (s.q0 + (lo - start)) * p.st[which ? 4 : 2];
     const int64_t tstride = p.st[which ? 4 : 2];
-    const int njobs = (hi - lo) * jn;
+    const int njobs = max(0, hi - lo) * jn;
     auto job = [&](int w, float* y, int& row, int& o0, int& o1) {
         row = w / jn;
-        const int64_t tok = s.q0 + (lo - start) + row;
         const int64_t a = static_cast<int64_t>(lo + row) * p.half;
-        row_job<T, VE, true>(p, src0 + tok * tstride, w - row * jn, !which, p.cos + a, p.sin + a, y,
+        row_job<T, VE, true>(p, src0 + row * tstride, w - row * jn, !which, p.cos + a, p.sin + a, y,
                              o0, o1);
     };
-    uint32_t most = 0;  // the largest finite |value|, as its bits
-    for (int w = threadIdx.x; w < njobs; w += blockDim.x) {
-        float y[2 * VE];
-        int row, o0, o1;
-        job(w, y, row, o0, o1);
+    auto largest = [&](const float* y, int o1, uint32_t most) {  // finite |value|, as its bits
 #pragma unroll
         for (int e = 0; e < 2 * VE; ++e) {
             const uint32_t v = __float_as_uint(y[e]) & 0x7fffffffu;
             if ((e < VE || o1 >= 0) && v < 0x7f800000u) most = max(most, v);
         }
+        return most;
+    };
+    // the first jobs of a thread stay in registers for the second pass (all of
+    // them, up to 1024 values of 16 bits a warp's worth of lanes); the rest is formed again
+    constexpr int kKeep = 2;
+    const int nth = blockDim.x;
+    float y[kKeep][2 * VE];
+    int row[kKeep], o0[kKeep], o1[kKeep];
+    uint32_t most = 0;
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+        const int w = threadIdx.x + u * nth;
+        if (w < njobs) {
+            job(w, y[u], row[u], o0[u], o1[u]);
+            most = largest(y[u], o1[u], most);
+        }
     }
+    for (int w = threadIdx.x + kKeep * nth; w < njobs; w += nth) {
+        float z[2 * VE];
+        int r, a0, a1;
+        job(w, z, r, a0, a1);
+        most = largest(z, a1, most);
+    }
+    if (append_bad_ids(p, b, s)) {
+        if (threadIdx.x == 0 && ib == 0 && p.status) atomicOr(p.status, KVC_DEV_OVERFLOW);
+        return;
+    }
+    if (lo >= hi) return;
+    const int64_t unit = static_cast<int64_t>(p.table[b * p.max_blocks + i]) * p.Hk + hk;
+    float* sp = (which ? p.value_scale : p.key_scale) + unit;
+    const int held = lo - i * p.bs;  // rows that the block already holds
+    const float old = held ? *sp : 0.f;
     most = __reduce_max_sync(0xffffffffu, most);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kAppThreads / 32; ++w) most = max(most, red[w]);
+    for (int w = 0; w < nth / 32; ++w) most = max(most, red[w]);
     int e = static_cast<int>(most >> 23) - 127 - Eight<E5M2>::top +
             ((most & 0x7fffffu) > 0x600000u ? 1 : 0);
     e = max(-100, min(100, e));
@@ -295,9 +349,8 @@ __device__ void append_block8(const AppendParams& p, int64_t idx) {
     if (held && old != scale) {  // the held rows, at the larger scale
         const float f = __fdiv_rn(old, scale);
         const int n = held * width;
-        for (int w = 2 * threadIdx.x; w + 1 < n; w += 2 * blockDim.x) {
-            const float2 v = from_eight2<E5M2>(*reinterpret_cast<const uint8_t*>(base + w) |
-                                               (static_cast<uint32_t>(base[w + 1]) << 8));
+        for (int w = 2 * threadIdx.x; w + 1 < n; w += 2 * nth) {
+            const float2 v = from_eight2<E5M2>(base[w] | (static_cast<uint32_t>(base[w + 1]) << 8));
             const uint32_t c = to_eight2<E5M2>(v.x * f, v.y * f);
             base[w] = static_cast<uint8_t>(c);
             base[w + 1] = static_cast<uint8_t>(c >> 8);
@@ -307,14 +360,20 @@ __device__ void append_block8(const AppendParams& p, int64_t idx) {
                 to_eight2<E5M2>(from_eight(base[n - 1], E5M2) * f, 0.f));
     }
     base += static_cast<int64_t>(held) * width;
-    for (int w = threadIdx.x; w < njobs; w += blockDim.x) {
-        float y[2 * VE];
-        int row, o0, o1;
-        job(w, y, row, o0, o1);
+    auto put = [&](float* z, int r, int a0, int a1) {
 #pragma unroll
-        for (int k = 0; k < 2 * VE; ++k) y[k] = pow2 ? y[k] * inv : __fdiv_rn(y[k], scale);
-        store_eight<VE, E5M2>(base + static_cast<int64_t>(row) * width + o0, y);
-        if (o1 >= 0) store_eight<VE, E5M2>(base + static_cast<int64_t>(row) * width + o1, y + VE);
+        for (int k = 0; k < 2 * VE; ++k) z[k] = pow2 ? z[k] * inv : __fdiv_rn(z[k], scale);
+        store_eight<VE, E5M2>(base + static_cast<int64_t>(r) * width + a0, z);
+        if (a1 >= 0) store_eight<VE, E5M2>(base + static_cast<int64_t>(r) * width + a1, z + VE);
+    };
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u)
+        if (static_cast<int>(threadIdx.x) + u * nth < njobs) put(y[u], row[u], o0[u], o1[u]);
+    for (int w = threadIdx.x + kKeep * nth; w < njobs; w += nth) {
+        float z[2 * VE];
+        int r, a0, a1;
+        job(w, z, r, a0, a1);
+        put(z, r, a0, a1);
     }
     if (threadIdx.x == 0) *sp = scale;
 }
@@ -324,7 +383,7 @@ __global__ void __launch_bounds__(kAppThreads) append_rotary_kernel(const __grid
     if (blockIdx.x < p.tok_blocks) {
         append_tokens<T, KIND != 0, VE>(p);
         if (blockIdx.x == 0 && p.status)  // sequences whose packed rows are no rows of the tensor
-            for (int64_t b = threadIdx.x; b < p.B; b += kAppThreads)
+            for (int64_t b = threadIdx.x; b < p.B; b += blockDim.x)
                 if (!paged_seq(p.cu, p.kl, b, p.total_q, p.max_q, p.M).ok)
                     atomicOr(p.status, KVC_DEV_OVERFLOW);
     } else if constexpr (KIND != 0) {
@@ -338,9 +397,9 @@ __global__ void __launch_bounds__(kAppThreads) append_rotary_kernel(const __grid
 template <typename T, int VE>
 cudaError_t launch_ve(const AppendParams& p, int kind, unsigned grid, cudaStream_t stream) {
     switch (kind) {
-        case 0: append_rotary_kernel<T, 0, VE><<<grid, kAppThreads, 0, stream>>>(p); break;
-        case 1: append_rotary_kernel<T, 1, VE><<<grid, kAppThreads, 0, stream>>>(p); break;
-        default: append_rotary_kernel<T, 2, VE><<<grid, kAppThreads, 0, stream>>>(p); break;
+        case 0: append_rotary_kernel<T, 0, VE><<<grid, p.threads, 0, stream>>>(p); break;
+        case 1: append_rotary_kernel<T, 1, VE><<<grid, p.threads, 0, stream>>>(p); break;
+        default: append_rotary_kernel<T, 2, VE><<<grid, p.threads, 0, stream>>>(p); break;
     }
     return cudaGetLastError();
 }

@@ -15,7 +15,7 @@ from typing import Optional
 
 import torch
 
-from .kvc import DTYPES, KvcError, _p, default_scale, library, status_string
+from .kvc import DTYPES, KvcError, default_scale, library, status_string
 
 #: pool types in 8 bits, kept with one fp32 scale for each (block, head)
 EIGHT_BIT = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
@@ -28,9 +28,13 @@ class PagedDims(ctypes.Structure):
                  "max_blocks")] + [("dtype", ctypes.c_int32), ("pool_dtype", ctypes.c_int32)]
 
 
+_lib = None
+
+
 def _paged_library() -> ctypes.CDLL:
-    lib = library()
-    if not getattr(lib, "_paged_ready", False):
+    global _lib
+    if _lib is None:
+        lib = library()
         vp, i64, i32, f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double
         dp, sp = ctypes.POINTER(PagedDims), ctypes.POINTER(ctypes.c_int64)
         lib.kvc_append_rotary_paged.restype = ctypes.c_int
@@ -42,8 +46,8 @@ def _paged_library() -> ctypes.CDLL:
         lib.kvc_attend_paged.restype = ctypes.c_int
         lib.kvc_attend_paged.argtypes = ([dp, sp] + [vp] * 8 + [f64, f64, vp, i64, vp, vp,
                                                                ctypes.c_size_t, vp, vp])
-        lib._paged_ready = True
-    return lib
+        _lib = lib
+    return _lib
 
 
 def make_paged_dims(B, total_q, max_q, Hq, Hk, D, Dv, num_blocks, block_size, max_blocks, dtype,
@@ -67,65 +71,89 @@ def attend_paged_workspace_bytes(dims: PagedDims) -> int:
     return int(_paged_library().kvc_attend_paged_workspace_bytes(ctypes.byref(dims)))
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr() or None
+
+
 def _ints(t: torch.Tensor, name: str, shape, device) -> torch.Tensor:
-    if t.dtype.is_floating_point or t.dtype == torch.bool or tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.dtype.is_floating_point or t.dtype == torch.bool:
         raise ValueError(f"{name} must be integers of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    return t.to(torch.int32).contiguous()
+    if t.dtype != torch.int32:
+        t = t.to(torch.int32)
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _check(packed, key_pool, value_pool, key_scale, value_scale, block_table, cu_seqlens_q,
            seqlens_k, what):
-    """The shared contract: types, devices, pool and table shapes. Returns the
-    int32 tables."""
+    """The shared contract: types, devices, pool and table shapes. Returns
+    (int32 tables, (T, Hq, D), (num_blocks, Hk, block_size, Dv))."""
     q = packed[0][1]
+    dtype, dev = q.dtype, q.device
+    grad = torch.is_grad_enabled()
     for name, t in packed:
         if t.dim() != 3:
             raise ValueError(f"{name} must be 3-D (tokens, heads, width), got {tuple(t.shape)}")
-        if t.dtype not in DTYPES or t.dtype != q.dtype:
+        if t.dtype != dtype or dtype not in DTYPES:
             raise ValueError(f"{name}: one dtype among float32/bfloat16/float16 is needed")
-        if t.device != q.device:
+        if t.device != dev:
             raise ValueError("all tensors must be on one device")
-    if q.device.type != "cuda":
+        if grad and t.requires_grad:
+            raise ValueError(f"{what} has no gradients: call it under torch.no_grad()")
+    if dev.type != "cuda":
         raise ValueError(f"{what} runs on a CUDA device only (no CPU path)")
-    if torch.is_grad_enabled() and any(t.requires_grad for _, t in packed):
-        raise ValueError(f"{what} has no gradients: call it under torch.no_grad()")
+    pool = key_pool.dtype
+    if pool != dtype and pool not in EIGHT_BIT:
+        raise ValueError("the pools are of the inputs' dtype, float8_e4m3fn or float8_e5m2")
     for name, t in (("key_pool", key_pool), ("value_pool", value_pool)):
         if t.dim() != 4:
             raise ValueError(f"{name} must be [num_blocks, Hk, block_size, width]")
-        if t.dtype != key_pool.dtype or (t.dtype != q.dtype and t.dtype not in EIGHT_BIT):
-            raise ValueError("the pools are of the inputs' dtype, float8_e4m3fn or float8_e5m2")
-        if t.device != q.device:
-            raise ValueError("all tensors must be on one device")
+        if t.dtype != pool or t.device != dev:
+            raise ValueError("the pools need one dtype and the inputs' device")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    T, Hq, Dq = q.shape
     nb, Hk, bs, D = key_pool.shape
-    if tuple(value_pool.shape[:3]) != (nb, Hk, bs):
+    vb, vh, vs, Dv = value_pool.shape
+    if (vb, vh, vs) != (nb, Hk, bs):
         raise ValueError("the pools' blocks, heads and block sizes differ")
-    if min(nb, Hk, bs, D, value_pool.shape[3]) < 1 or q.shape[1] < 1 or q.shape[1] % Hk:
+    if min(nb, Hk, bs, D, Dv, Hq) < 1 or Hq % Hk:
         raise ValueError("need sizes >= 1 and Hq a multiple of Hk")
-    if max(D, value_pool.shape[3]) > 256:
+    if D > 256 or Dv > 256:
         raise ValueError("widths up to 256 are supported")
-    if q.shape[2] != D:
+    if Dq != D:
         raise ValueError("the query's width is not the key pool's")
-    for name, t in (("key_scale", key_scale), ("value_scale", value_scale)):
-        if key_pool.dtype not in EIGHT_BIT:
-            if t is not None:
-                raise ValueError(f"{name} goes with an 8-bit pool only")
-            continue
-        if t is None or t.dtype != torch.float32 or tuple(t.shape) != (nb, Hk):
-            raise ValueError(f"an 8-bit pool needs {name}: float32 [num_blocks, Hk]")
-        if t.device != q.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous on the pool's device")
-    if block_table.dim() != 2 or block_table.shape[1] < 1:
+    if pool in EIGHT_BIT:
+        for name, t in (("key_scale", key_scale), ("value_scale", value_scale)):
+            if t is None or t.dtype != torch.float32 or t.shape != (nb, Hk):
+                raise ValueError(f"an 8-bit pool needs {name}: float32 [num_blocks, Hk]")
+            if t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous on the pool's device")
+    elif key_scale is not None or value_scale is not None:
+        raise ValueError("key_scale / value_scale go with an 8-bit pool only")
+    if block_table.dim() != 2 or min(block_table.shape) < 1:
         raise ValueError("block_table must be [B, max_blocks]")
     B = block_table.shape[0]
-    if B < 1:
-        raise ValueError("need B >= 1")
-    return (_ints(block_table, "block_table", block_table.shape, q.device),
-            _ints(cu_seqlens_q, "cu_seqlens_q", (B + 1,), q.device),
-            _ints(seqlens_k, "seqlens_k", (B,), q.device))
+    return ((_ints(block_table, "block_table", block_table.shape, dev),
+             _ints(cu_seqlens_q, "cu_seqlens_q", (B + 1,), dev),
+             _ints(seqlens_k, "seqlens_k", (B,), dev)), (T, Hq, D), (nb, Hk, bs, Dv))
+
+
+class _OnDevice:
+    """The inputs' device as the current one, where it is not already."""
+
+    def __init__(self, device):
+        index = device.index
+        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _max_q(max_seqlen_q, cu, total_q) -> int:
@@ -145,7 +173,7 @@ def _packed(t: torch.Tensor) -> torch.Tensor:
 def _output(out, shape, like, name):
     if out is None:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != like.dtype or out.device != like.device \
+    if out.shape != shape or out.dtype != like.dtype or out.device != like.device \
             or not out.is_contiguous():
         raise ValueError(f"{name} must be contiguous {tuple(shape)} of the inputs' dtype and device")
     return out
@@ -189,13 +217,10 @@ def append_rotary_paged(query: torch.Tensor, new_key: torch.Tensor, new_value: t
     ``status``: an int32 CUDA tensor into which KVC_DEV bits are OR-ed. Sequences
     must write distinct blocks. No gradients (inputs that ask for them are refused).
     """
-    table, cu, kl = _check((("query", query), ("new_key", new_key), ("new_value", new_value)),
-                           key_pool, value_pool, key_scale, value_scale, block_table, cu_seqlens_q,
-                           seqlens_k, "append_rotary_paged")
-    T, Hq, D = query.shape
-    nb, Hk, bs, _ = key_pool.shape
-    Dv = value_pool.shape[3]
-    if tuple(new_key.shape) != (T, Hk, D) or tuple(new_value.shape) != (T, Hk, Dv):
+    (table, cu, kl), (T, Hq, D), (nb, Hk, bs, Dv) = _check(
+        (("query", query), ("new_key", new_key), ("new_value", new_value)), key_pool, value_pool,
+        key_scale, value_scale, block_table, cu_seqlens_q, seqlens_k, "append_rotary_paged")
+    if new_key.shape != (T, Hk, D) or new_value.shape != (T, Hk, Dv):
         raise ValueError(f"new_key / new_value must be {(T, Hk, D)} / {(T, Hk, Dv)}")
     for name, t in (("cos", cos), ("sin", sin)):
         if t.dim() != 2 or t.dtype != torch.float32 or t.shape != cos.shape:
@@ -211,14 +236,14 @@ def append_rotary_paged(query: torch.Tensor, new_key: torch.Tensor, new_value: t
     out = _output(out_query, (T, Hq, D), query, "out_query")
     dims = make_paged_dims(table.shape[0], T, max_q, Hq, Hk, D, Dv, nb, bs, table.shape[1],
                            query.dtype, key_pool.dtype)
-    st = (ctypes.c_int64 * 6)(*(x for t in (q, k, v) for x in t.stride()[:2]))
-    with torch.cuda.device(query.device):
-        stream = torch.cuda.current_stream(query.device).cuda_stream
+    st = (ctypes.c_int64 * 6)(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2])
+    status = _ptr(_status(status, query.device))
+    with _OnDevice(query.device):
         rc = lib.kvc_append_rotary_paged(
-            ctypes.byref(dims), 2 * c.shape[1], c.shape[0], int(bool(interleaved)), st, _p(q),
-            _p(k), _p(v), _p(table), _p(cu), _p(kl), _p(c), _p(s), _p(key_pool), _p(value_pool),
-            _p(key_scale), _p(value_scale), _p(out), _p(_status(status, query.device)),
-            ctypes.c_void_p(stream))
+            ctypes.byref(dims), 2 * c.shape[1], c.shape[0], int(bool(interleaved)), st, _ptr(q),
+            _ptr(k), _ptr(v), _ptr(table), _ptr(cu), _ptr(kl), _ptr(c), _ptr(s), _ptr(key_pool),
+            _ptr(value_pool), _ptr(key_scale), _ptr(value_scale), _ptr(out), status,
+            torch.cuda.current_stream(query.device).cuda_stream)
     if rc != 0:
         raise KvcError(rc, status_string(rc))
     return {"query": out, "key_pool": key_pool, "value_pool": value_pool, "key_scale": key_scale,
@@ -251,11 +276,9 @@ def attention_over_paged_cache(q: torch.Tensor, key_pool: torch.Tensor, value_po
     cu_seqlens_q when not given (a device sync). No gradients (inputs that ask
     for them are refused).
     """
-    table, cu, kl = _check((("q", q),), key_pool, value_pool, key_scale, value_scale, block_table,
-                           cu_seqlens_q, seqlens_k, "attention_over_paged_cache")
-    T, Hq, D = q.shape
-    nb, Hk, bs, _ = key_pool.shape
-    Dv = value_pool.shape[3]
+    (table, cu, kl), (T, Hq, D), (nb, Hk, bs, Dv) = _check(
+        (("q", q),), key_pool, value_pool, key_scale, value_scale, block_table, cu_seqlens_q,
+        seqlens_k, "attention_over_paged_cache")
     scale = default_scale(D) if scale is None else float(scale)
     if not (scale > 0.0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
@@ -283,13 +306,13 @@ def attention_over_paged_cache(q: torch.Tensor, key_pool: torch.Tensor, value_po
             not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     st = (ctypes.c_int64 * 2)(*qq.stride()[:2])
-    with torch.cuda.device(q.device):
-        stream = torch.cuda.current_stream(q.device).cuda_stream
+    status = _ptr(_status(status, q.device))
+    with _OnDevice(q.device):
         rc = lib.kvc_attend_paged(
-            ctypes.byref(dims), st, _p(qq), _p(key_pool), _p(value_pool), _p(key_scale),
-            _p(value_scale), _p(table), _p(cu), _p(kl), ctypes.c_double(scale),
-            ctypes.c_double(softcap), _p(alibi_slopes), window, _p(out), _p(workspace),
-            workspace.numel(), _p(_status(status, q.device)), ctypes.c_void_p(stream))
+            ctypes.byref(dims), st, _ptr(qq), _ptr(key_pool), _ptr(value_pool), _ptr(key_scale),
+            _ptr(value_scale), _ptr(table), _ptr(cu), _ptr(kl), scale, softcap,
+            _ptr(alibi_slopes), window, _ptr(out), _ptr(workspace), workspace.numel(), status,
+            torch.cuda.current_stream(q.device).cuda_stream)
     if rc != 0:
         raise KvcError(rc, status_string(rc))
     return out
