@@ -176,6 +176,7 @@ struct AppendParams {
     void* out_query;
     int32_t* status;
     int threads;          // of a block
+    int hg;               // heads of a thread's turn: 1 or 4
     int tpb;              // tokens per block of the first tok_blocks blocks
     unsigned tok_blocks;
     int64_t seq_blocks;   // 8-bit pools: pool blocks a sequence can touch

@@ -298,15 +298,14 @@ int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int6
     };
     while (ve > 1 && !fits(ve)) ve = ve == 8 ? 4 : 1;
     // a block per token while blocks are few; then several, so that the look-up of
-    // a token's sequence and slot is paid for once per block's worth of loads
-    p.tpb = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxTokensPerBlock,
-                                                                    T / (8 * kPlanSms))));
+    // a token's sequence and slot is paid for once per block's worth of loads, but
+    // enough blocks for several rounds on every SM
+    p.tpb = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, T / (8 * kPlanSms))));
     p.tok_blocks = static_cast<unsigned>((T + p.tpb - 1) / p.tpb);
-    p.threads = 256;
+    p.hg = T <= 2 * kPlanSms ? 1 : 4;
+    // 8-bit pools: small blocks, more of them on an SM (their two passes meet at barriers)
+    p.threads = eight(d) && std::max(d.D - half, d.Dv) / ve <= 128 ? 128 : 256;
     if (eight(d)) {
-        // a block's second pass takes up to two jobs of a thread out of registers
-        const int64_t row_jobs = std::max((d.D - half) / ve, d.Dv / ve);
-        if (row_jobs <= 128 && std::min(d.max_q, d.block_size) * row_jobs <= 256) p.threads = 128;
         p.seq_blocks = std::min<int64_t>((d.max_q + d.block_size - 2) / d.block_size + 1, d.max_blocks);
         p.units8 = d.B * p.seq_blocks * d.Hk * 2;
     }

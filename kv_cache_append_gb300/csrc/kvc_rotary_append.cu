@@ -13,8 +13,8 @@
 // inputs' type, write the keys and values, each a pure stream: every byte is
 // read and written once); with an 8-bit pool the remaining blocks each take one
 // (sequence, touched pool block, head, keys or values): a pass over the block's
-// new rows for the largest absolute value, the block's scale, and a second pass,
-// out of registers, that rounds and stores.
+// new rows for the largest absolute value, the block's scale, and a second pass
+// that rounds and stores.
 //
 // 8-bit pools: the scale is 2^e, e the least with amax <= 1.75 * 2^top * 2^e,
 // never below the scale of rows that the block already holds; a power of two
@@ -162,39 +162,94 @@ __device__ __forceinline__ bool append_bad_ids(const AppendParams& p, int64_t b,
     return __syncthreads_or(bad);
 }
 
-// Rows of `heads` heads for each of the block's tokens: a thread keeps one job of
-// a row and steps over the rows, so that nothing is divided in the loop.
+// Rows of `heads` heads for each of the block's tokens: a thread takes one job of
+// the rows of p.hg heads (kHeads, or one where tokens are few), whose loads are
+// all under way together and share the angles (one row at a time, the loads' latency held a prompt to 38% of the
+// copy bandwidth), and steps over such groups, so that nothing is divided in the loop.
+constexpr int kHeads = 4;
 template <typename T, int VE, typename Dst>
 __device__ __forceinline__ void token_rows(const AppendParams& p, const T* src, int64_t tok0, int nt,
                                            int heads, int jobs, int64_t st_tok, int64_t st_head,
-                                           bool rotate, const int* pos, bool zero_bad, Dst dst_of) {
+                                           bool rotate, const int* pos, bool zero_bad, int first, Dst dst_of) {
+    using W = typename Word<VE * sizeof(T)>::type;
+    const int groups = (heads + p.hg - 1) / p.hg;  // of a token
     const int step = blockDim.x / jobs;
-    int h = threadIdx.x / jobs;
-    if (h >= step) return;
-    const int j = threadIdx.x - h * jobs;
+    // the work starts at thread `first`: behind what the rows before have left idle
+    int tid = threadIdx.x - first;
+    if (tid < 0) tid += blockDim.x;
+    int g = tid / jobs;
+    if (g >= step) return;
+    const int j = tid - g * jobs;
+    const int npair = rotate ? p.half / VE : 0;
+    const bool turn = j < npair;
+    int o0, o1 = 0;
+    if (!turn) {
+        o0 = (rotate ? 2 * p.half : 0) + (j - npair) * VE;
+    } else {
+        o0 = p.interleaved ? 2 * j * VE : j * VE;
+        o1 = p.interleaved ? o0 + VE : p.half + j * VE;
+    }
     int i = 0;
     for (;;) {
-        while (h >= heads) {
-            h -= heads;
+        while (g >= groups) {
+            g -= groups;
             ++i;
         }
         if (i >= nt) return;
         const int at = pos[i];  // -1: outside the contract, -2: of no sequence
         if (at >= 0 || (at == -1 && zero_bad)) {
-            const int64_t a = static_cast<int64_t>(max(at, 0)) * p.half;
-            float y[2 * VE];
-            int o0, o1;
-            row_job<T, VE, false>(p, src + (tok0 + i) * st_tok + h * st_head, j, rotate, p.cos + a,
-                                  p.sin + a, y, o0, o1);
-            if (at < 0) {
+            const int h0 = g * p.hg, n = min(p.hg, heads - h0);
+            const T* row = src + (tok0 + i) * st_tok + h0 * st_head;
+            W x0[kHeads], x1[kHeads];
 #pragma unroll
-                for (int e = 0; e < 2 * VE; ++e) y[e] = 0.f;
+            for (int u = 0; u < kHeads; ++u)
+                if (u < n) {
+                    x0[u] = *reinterpret_cast<const W*>(row + u * st_head + o0);
+                    if (turn) x1[u] = *reinterpret_cast<const W*>(row + u * st_head + o1);
+                }
+            float c[VE], sn[VE];
+            if (turn) {
+                const int64_t a = static_cast<int64_t>(max(at, 0)) * p.half + j * VE;
+                load_angles<VE>(p.cos + a, c);
+                load_angles<VE>(p.sin + a, sn);
             }
-            T* dst = dst_of(i, h);
-            store_vec<T, VE>(dst + o0, y);
-            if (o1 >= 0) store_vec<T, VE>(dst + o1, y + VE);
+#pragma unroll
+            for (int u = 0; u < kHeads; ++u) {
+                if (u >= n) break;
+                T* dst = dst_of(i, h0 + u);
+                if (at < 0) {
+                    float z[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) z[e] = 0.f;
+                    store_vec<T, VE>(dst + o0, z);
+                    if (turn) store_vec<T, VE>(dst + o1, z);
+                } else if (!turn) {
+                    *reinterpret_cast<W*>(dst + o0) = x0[u];
+                } else {
+                    const T* e0 = reinterpret_cast<const T*>(&x0[u]);
+                    const T* e1 = reinterpret_cast<const T*>(&x1[u]);
+                    float y[2 * VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        auto el = [&](int k) {
+                            return Storage<T>::to_float(k < VE ? e0[k] : e1[k - VE]);
+                        };
+                        if (p.interleaved) {
+                            const float a = el(2 * e), b = el(2 * e + 1);
+                            y[2 * e] = fmaf(a, c[e], -b * sn[e]);
+                            y[2 * e + 1] = fmaf(b, c[e], a * sn[e]);
+                        } else {
+                            const float a = el(e), b = el(VE + e);
+                            y[e] = fmaf(a, c[e], -b * sn[e]);
+                            y[VE + e] = fmaf(b, c[e], a * sn[e]);
+                        }
+                    }
+                    store_vec<T, VE>(dst + o0, y);
+                    store_vec<T, VE>(dst + o1, y + VE);
+                }
+            }
         }
-        h += step;
+        g += step;
     }
 }
 
@@ -240,17 +295,20 @@ __device__ void append_tokens(const AppendParams& p) {
     __syncthreads();
     const int jr = (p.half + (p.D - 2 * p.half)) / VE, jv = p.Dv / VE;
     token_rows<T, VE>(p, static_cast<const T*>(p.query), tok0, nt, p.Hq, jr, p.st[0], p.st[1], true,
-                      pos, true, [&](int i, int h) {
+                      pos, true, 0, [&](int i, int h) {
                           return static_cast<T*>(p.out_query) + ((tok0 + i) * p.Hq + h) * p.D;
                       });
     if (EIGHT) return;
+    const int kv_groups = nt * ((p.Hk + p.hg - 1) / p.hg);
+    const int k_at = nt * ((p.Hq + p.hg - 1) / p.hg) * jr % blockDim.x;
+    const int v_at = (k_at + kv_groups * jr) % blockDim.x;
     token_rows<T, VE>(p, static_cast<const T*>(p.new_key), tok0, nt, p.Hk, jr, p.st[2], p.st[3], true,
-                      pos, false, [&](int i, int h) {
+                      pos, false, k_at, [&](int i, int h) {
                           return static_cast<T*>(p.key_pool) +
                                  (dst_row[i] + static_cast<int64_t>(h) * p.bs) * p.D;
                       });
     token_rows<T, VE>(p, static_cast<const T*>(p.new_value), tok0, nt, p.Hk, jv, p.st[4], p.st[5],
-                      false, pos, false, [&](int i, int h) {
+                      false, pos, false, v_at, [&](int i, int h) {
                           return static_cast<T*>(p.value_pool) +
                                  (dst_row[i] + static_cast<int64_t>(h) * p.bs) * p.Dv;
                       });
@@ -304,8 +362,8 @@ __device__ void append_block8(const AppendParams& p, int64_t unit_index) {
         }
         return most;
     };
-    // the first jobs of a thread stay in registers for the second pass (all of
-    // them, up to 1024 values of 16 bits a warp's worth of lanes); the rest is formed again
+    // a thread's first jobs stay in registers for the second pass (all there is for
+    // small pool blocks); the rest is formed again, out of L1
     constexpr int kKeep = 2;
     const int nth = blockDim.x;
     float y[kKeep][2 * VE];
@@ -379,7 +437,7 @@ __device__ void append_block8(const AppendParams& p, int64_t unit_index) {
 }
 
 template <typename T, int KIND, int VE>  // KIND 0: a pool of the inputs' type, 1: e4m3, 2: e5m2
-__global__ void __launch_bounds__(kAppThreads) append_rotary_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppThreads, 3) append_rotary_kernel(const __grid_constant__ AppendParams p) {
     if (blockIdx.x < p.tok_blocks) {
         append_tokens<T, KIND != 0, VE>(p);
         if (blockIdx.x == 0 && p.status)  // sequences whose packed rows are no rows of the tensor
