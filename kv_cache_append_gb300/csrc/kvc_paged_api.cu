@@ -159,7 +159,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
     auto layout = [&](int64_t stages, int64_t cap) {  // scales, items, exchange, queries, weights, stages
         p.off_item = static_cast<int>(512 + std::max<int64_t>(320, stages * 256));
         p.off_x = p.off_item + 128 + 2 * 384;
-        p.off_q = static_cast<int>(up(p.off_x + 2 * t.nr * 16 + 32, 1024));
+        p.off_q = static_cast<int>(up(p.off_x + 2 * t.nr * 16 + 64, 1024));
         p.off_p = p.off_q + p.ni * p.q_bytes;
         p.off_stage = static_cast<int>(p.off_p + npt * (es == 1 ? 3 : 2) * nblk);
         p.ns = static_cast<int>(std::min(stages, (cap - p.off_stage) / p.stage_bytes));

@@ -25,7 +25,8 @@
 // The further parts cost nothing that matters: the tensor cores are idle most of
 // the time.
 //
-// Warps: 4 softmax warps (a thread owns a slot), one S issuer, one P.V issuer,
+// Warps: one or two groups of 4 softmax warps (a thread owns a slot, for all rows
+// or for its group's half of them), one S issuer, one P.V issuer,
 // one producer (block-table look-ups, scales, TMA boxes), one scheduler, which walks
 // the block's runs (kvc_paged_tc.cuh) and splits the next run's query rows
 // while the others work on the current one. 8-bit tiles of D = Dv = 128 are 32
@@ -46,8 +47,13 @@ namespace kvc {
 namespace {
 
 constexpr int kTS = 128;
-constexpr int kMmaWarp = 4, kPvWarp = 5, kProdWarp = 6;  // warp 7 schedules
-constexpr int kThreads = 8 * 32;
+// SG groups of 4 softmax warps (each takes NR / SG of the unit's rows for all 128
+// slots), then the S issuer, the P.V issuer, the producer and the scheduler.
+template <int SG>
+struct Roles {
+    static constexpr int soft = 4 * SG, s = soft, pv = soft + 1, prod = soft + 2;
+    static constexpr int threads = (soft + 4) * 32;
+};
 struct Bars {
     uint32_t base;
     __device__ uint32_t full(int s) const { return base + 8u * s; }
@@ -58,10 +64,10 @@ struct Bars {
     __device__ uint32_t s_free(int b) const { return base + 208u + 8u * b; }
     __device__ uint32_t p_ready(int b) const { return base + 224u + 8u * b; }
     __device__ uint32_t o_done(int b) const { return base + 240u + 8u * b; }
-    __device__ uint32_t meet() const { return base + 256u; }
-    __device__ uint32_t drained() const { return base + 264u; }
+    __device__ uint32_t meet(int g) const { return base + 256u + 8u * g; }
+    __device__ uint32_t drained() const { return base + 272u; }
 };
-constexpr int kTmemSlot = 272, kAbort = 276, kBad = 280 /* [4] */, kOdd = 296 /* [2] */;
+constexpr int kTmemSlot = 280, kAbort = 284, kBad = 288 /* [4] */, kOdd = 304 /* [2] */;
 // from 512: PagedStart (read before the first tile is loaded), then the stages'
 // StageScales; then the items and their rows' data
 
@@ -339,21 +345,23 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
     warp_wait(bars.drained(), 0u, &never);
 }
 
-template <typename T, int EB, int NR, bool MOD>
+template <typename T, int EB, int NRT, int SG, bool MOD>
 __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars bars,
                               volatile int* abort, uint32_t tmem, const PagedStart* st) {
-    constexpr int DN = NR <= 16 ? 16 : 32;
+    constexpr int DN = NRT <= 16 ? 16 : 32;
+    constexpr int NR = NRT / SG;  // rows of this thread's group
     using S = Shape<EB, DN>;
     using St = Storage<T>;
     const PagedAttendParams& a = p.a;
     const int t = threadIdx.x & 127;  // slot of the tile; value column of O^T
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int g = threadIdx.x >> 7, r0 = g * NR;  // group, its first row
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16) + r0;
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
     const StageScales* scales = reinterpret_cast<const StageScales*>(smem + 512);
-    // exchange: values [2][NR][4], flags [2][4]
-    float* xval = reinterpret_cast<float*>(smem + p.off_x);
-    int* xflag = reinterpret_cast<int*>(smem + p.off_x + 2 * NR * 4 * 4);
+    // the group's exchange: values [2][NR][4], flags [2][4]
+    float* xval = reinterpret_cast<float*>(smem + p.off_x + g * (2 * NR * 16 + 32));
+    int* xflag = reinterpret_cast<int*>(xval + 2 * NR * 4);
     unsigned char* pt = smem + p.off_p;
     const int nkb = (a.D * EB + 127) / 128;
     constexpr int nvb = EB == 1 ? 1 : 2;
@@ -368,8 +376,8 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
     // exchange buffer rv % 2 before is visible to all after.
     auto meet = [&]() -> bool {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.meet(), 1u);
-        const bool ok = warp_wait(bars.meet(), rv & 1u, abort);
+        if (lane == 0) mbar_arrive(bars.meet(g), 1u);
+        const bool ok = warp_wait(bars.meet(g), rv & 1u, abort);
         ++rv;
         return ok;
     };
@@ -423,14 +431,14 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 seen = 0u;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    const int lim = rd->lim[r];
+                    const int lim = rd->lim[r0 + r];
                     if (j <= lim && (a.window == 0 || j > lim - a.window)) seen |= 1u << r;
                 }
             }
             bool need = false;
 #pragma unroll
             for (int r = 0; r < NR; r += 4) {
-                const float4 m4 = *reinterpret_cast<const float4*>(rd->mul + r);
+                const float4 m4 = *reinterpret_cast<const float4*>(rd->mul + r0 + r);
                 const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -444,7 +452,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                         } else {
                             s *= kLog2e;
                         }
-                        s -= rd->slope[r + e] * static_cast<float>(rd->lim[r + e] - j);
+                        s -= rd->slope[r0 + r + e] * static_cast<float>(rd->lim[r0 + r + e] - j);
                     }
                     s += lv;
                     if (!((seen >> (r + e)) & 1u)) s = -INFINITY;
@@ -495,7 +503,8 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                     split_weights(sv[r], sv[r + 1], sv[r + 2], sv[r + 3], part);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        unsigned char* o = pb + (r + e) * 128 + (((t >> 4) ^ ((r + e) & 7)) << 4) + (t & 15);
+                        const int rr = r0 + r + e;
+                        unsigned char* o = pb + rr * 128 + (((t >> 4) ^ (rr & 7)) << 4) + (t & 15);
 #pragma unroll
                         for (int k2 = 0; k2 < 3; ++k2)
                             o[k2 * S::nblk] = static_cast<unsigned char>(part[k2] >> (8 * e));
@@ -504,11 +513,11 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             } else {
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
-                    *reinterpret_cast<T*>(pb + (t >> 6) * S::nblk + r * 128 +
-                                          ((((t & 63) >> 3) ^ (r & 7)) << 4) + (t & 7) * 2) =
+                    *reinterpret_cast<T*>(pb + (t >> 6) * S::nblk + (r0 + r) * 128 +
+                                          ((((t & 63) >> 3) ^ ((r0 + r) & 7)) << 4) + (t & 7) * 2) =
                         St::from_float(sv[r]);
             }
-            if (edge) {
+            if (edge && g == 0) {
                 unsigned char* vrow = smem + p.off_stage + static_cast<int64_t>(ring.s) * p.stage_bytes +
                                       nkb * kTS * 128 + t * 128;
                 const bool some = j <= it.last && j >= it.lo;
@@ -584,7 +593,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 if (fabsf(v) < INFINITY) continue;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    const int lim = rd->lim[r];
+                    const int lim = rd->lim[r0 + r];
                     if (j <= lim && (a.window == 0 || j > lim - a.window)) ov[r] += v;
                 }
             }
@@ -594,21 +603,21 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + ((it.flags & kItemBegins) ? 1 : 0);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            const int lim = rd->lim[r];
+            const int lim = rd->lim[r0 + r];
             if (lim < 0) continue;
             const float4 q4 = *reinterpret_cast<const float4*>(xval + (bm * NR + r) * 4);
             const float l = (q4.x + q4.y) + (q4.z + q4.w);
             if (whole) {
-                const int rr = it.r0 + r;
+                const int rr = it.r0 + r0 + r;
                 const int64_t row = static_cast<int64_t>(it.q0 + rr / a.G) * a.Hq + it.hk * a.G + rr % a.G;
                 if (t < a.Dv)
                     static_cast<T*>(a.out)[row * a.Dv + t] =
                         St::from_float(bad ? 0.f : __fdiv_rn(ov[r], l));
             } else {
-                if (t < a.Dv) p.part_acc[(slot * p.RG + r) * a.Dv + t] = ov[r];
+                if (t < a.Dv) p.part_acc[(slot * p.RG + r0 + r) * a.Dv + t] = ov[r];
                 if (t == r) {
-                    p.part_ml[2 * (slot * p.RG + r)] = mref[r];
-                    p.part_ml[2 * (slot * p.RG + r) + 1] = bad ? -1.f : l;
+                    p.part_ml[2 * (slot * p.RG + r0 + r)] = mref[r];
+                    p.part_ml[2 * (slot * p.RG + r0 + r) + 1] = bad ? -1.f : l;
                 }
             }
         }
@@ -619,11 +628,13 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
     }
 }
 
-template <typename T, int EB, int NR, bool MOD>
-__global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
+template <typename T, int EB, int NR, int SG, bool MOD>
+__global__ void __launch_bounds__(Roles<SG>::threads, EB == 1 && NR <= 16 ? 2 : 1)
     paged_decode_kernel(const __grid_constant__ PagedTcParams p) {
     constexpr int DN = NR <= 16 ? 16 : 32;
     using S = Shape<EB, DN>;
+    using R = Roles<SG>;
+    constexpr int kThreads = R::threads;
     extern __shared__ __align__(1024) unsigned char smem[];
     const Bars bars{smem_addr(smem)};
     volatile int* abort = reinterpret_cast<volatile int*>(smem + kAbort);
@@ -636,15 +647,15 @@ __global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
         }
         for (int k = 0; k < p.ni; ++k) {
             mbar_init(bars.item_full(k), 1u);
-            mbar_init(bars.item_empty(k), 3u + 4u);  // producer, both issuers, softmax warps
+            mbar_init(bars.item_empty(k), 3u + R::soft);  // producer, both issuers, softmax warps
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bars.s_ready(b), 1u);
-            mbar_init(bars.s_free(b), 4u);
-            mbar_init(bars.p_ready(b), 4u);
+            mbar_init(bars.s_free(b), R::soft);
+            mbar_init(bars.p_ready(b), R::soft);
             mbar_init(bars.o_done(b), 1u);
         }
-        mbar_init(bars.meet(), 4u);
+        for (int g = 0; g < SG; ++g) mbar_init(bars.meet(g), 4u);
         mbar_init(bars.drained(), 2u);
         *abort = 0;
         fence_mbar_init();
@@ -653,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
     for (int i = threadIdx.x; i < S::npt * S::pbytes / 16; i += kThreads)
         reinterpret_cast<uint4*>(smem + p.off_p)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_async_shared();
-    if (warp == kMmaWarp) {
+    if (warp == R::s) {
         tmem_alloc(smem_addr(smem + kTmemSlot), S::cols);
         tmem_relinquish();
     }
@@ -663,20 +674,20 @@ __global__ void __launch_bounds__(kThreads, EB == 1 && NR <= 16 ? 2 : 1)
     const uint32_t tmem = uniform(*reinterpret_cast<volatile int*>(smem + kTmemSlot));
     launch_dependents();
 
-    if (warp < 4) {
-        softmax_warps<T, EB, NR, MOD>(p, smem, bars, abort, tmem, st);
-    } else if (warp == kMmaWarp) {
+    if (warp < R::soft) {
+        softmax_warps<T, EB, NR, SG, MOD>(p, smem, bars, abort, tmem, st);
+    } else if (warp == R::s) {
         s_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
-    } else if (warp == kPvWarp) {
+    } else if (warp == R::pv) {
         pv_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
-    } else if (warp == kProdWarp) {
+    } else if (warp == R::prod) {
         producer_warp<EB>(p, smem, bars, abort);
     } else {
         sched_warp<T, EB, DN>(p, smem, bars, st, abort);
     }
     tc_fence_before();
     __syncthreads();  // every thread reaches this exactly once: all waits are bounded
-    if (warp == kMmaWarp) {
+    if (warp == R::s) {
         tc_fence_after();
         tmem_dealloc(tmem, S::cols);
     }
@@ -766,23 +777,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
     }
 }
 
-template <typename T, int EB, int NR, bool MOD>
+template <typename T, int EB, int NR, int SG, bool MOD>
 cudaError_t launch_t(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
-    auto kern = paged_decode_kernel<T, EB, NR, MOD>;
+    auto kern = paged_decode_kernel<T, EB, NR, SG, MOD>;
     static SmemLimit limit;
     cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern));
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(p.ctas), kThreads, smem, stream>>>(p);
+    kern<<<static_cast<unsigned>(p.ctas), Roles<SG>::threads, smem, stream>>>(p);
     return cudaGetLastError();
+}
+template <typename T, int EB, int NR>
+cudaError_t launch_nr(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
+    // where a block has the SM to itself, two softmax groups from 8 rows on
+    constexpr int SG = EB == 1 ? (NR == 32 ? 2 : 1) : (NR >= 8 ? 2 : 1);
+    return p.a.softcap > 0.f || p.a.slopes ? launch_t<T, EB, NR, SG, true>(p, smem, stream)
+                                           : launch_t<T, EB, NR, SG, false>(p, smem, stream);
 }
 template <typename T, int EB>
 cudaError_t launch_eb(const PagedTcParams& p, int nr, size_t smem, cudaStream_t stream) {
-    const bool mod = p.a.softcap > 0.f || p.a.slopes;
     switch (nr) {
-        case 4: return mod ? launch_t<T, EB, 4, true>(p, smem, stream) : launch_t<T, EB, 4, false>(p, smem, stream);
-        case 8: return mod ? launch_t<T, EB, 8, true>(p, smem, stream) : launch_t<T, EB, 8, false>(p, smem, stream);
-        case 16: return mod ? launch_t<T, EB, 16, true>(p, smem, stream) : launch_t<T, EB, 16, false>(p, smem, stream);
-        default: return mod ? launch_t<T, EB, 32, true>(p, smem, stream) : launch_t<T, EB, 32, false>(p, smem, stream);
+        case 4: return launch_nr<T, EB, 4>(p, smem, stream);
+        case 8: return launch_nr<T, EB, 8>(p, smem, stream);
+        case 16: return launch_nr<T, EB, 16>(p, smem, stream);
+        default: return launch_nr<T, EB, 32>(p, smem, stream);
     }
 }
 
