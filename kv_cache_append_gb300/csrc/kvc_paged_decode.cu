@@ -186,12 +186,12 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
         if (it.flags & kItemDone) break;
         int id = feed_id<kTS>(p, it, it.tile0);
         int id1 = it.nt > 1 ? feed_id<kTS>(p, it, it.tile0 + 1) : kNoBox;
-        float2 fs = make_float2(1.f, 1.f), fs1 = fs;
-        if (EB == 1) fs = feed_scales(p, it, id);
+        float fs = 1.f, fs1 = 1.f;
+        if (EB == 1) fs = feed_scale(p, it, id);
         for (int n = 0; n < it.nt; ++n) {
             const int tile = it.tile0 + n;
             const int id2 = n + 2 < it.nt ? feed_id<kTS>(p, it, tile + 2) : kNoBox;
-            if (EB == 1) fs1 = feed_scales(p, it, id1);
+            if (EB == 1) fs1 = feed_scale(p, it, id1);
             if (issued >= p.ns && !warp_wait(bars.empty(ring.s), ring.ph ^ 1u, abort)) {
                 ok = false;
                 break;
@@ -202,9 +202,8 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
             }
             if (EB == 1) feed_store(sc + ring.s, fs);
             const uint32_t sK = stage0 + static_cast<uint32_t>(ring.s) * p.stage_bytes;
-            feed_copy<EB, kTS>(p, it, &p.tk, tile, id, sK, nkb, bars.full(ring.s), true, nvb);
-            feed_copy<EB, kTS>(p, it, &p.tv, tile, id, sK + static_cast<uint32_t>(nkb * kTS * 128), nvb,
-                               bars.full(ring.s), false);
+            feed_copy<EB, kTS>(p, it, tile, id, sK, nkb, sK + static_cast<uint32_t>(nkb * kTS * 128), nvb,
+                               bars.full(ring.s));
             id = id1;
             id1 = id2;
             fs = fs1;

@@ -140,8 +140,8 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + kItems);
     StageScales* sc = reinterpret_cast<StageScales*>(smem + kScales);
     const int nkb = (a.D * EB + 127) / 128, nvb = (a.Dv * EB + 127) / 128;
-    const int nb = KEYS ? nkb : nvb, stages = KEYS ? p.ns : p.nv;
-    const uint32_t bytes = nb * kTS * 128;
+    const int stages = KEYS ? p.ns : p.nv;
+    const uint32_t bytes = (KEYS ? nkb : nvb) * kTS * 128;
     const uint32_t base = smem_addr(smem + p.off_stage) + (KEYS ? 0 : p.ns * nkb * kTS * 128);
     int c = 0;  // tiles issued
     Ring ring;
@@ -154,12 +154,12 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
         constexpr bool kScaled = EB == 1 && KEYS;
         int id = feed_id<kTS>(p, it, it.tile0);
         int id1 = it.nt > 1 ? feed_id<kTS>(p, it, it.tile0 + 1) : kNoBox;
-        float2 fs = make_float2(1.f, 1.f), fs1 = fs;
-        if (kScaled) fs = feed_scales(p, it, id);
+        float fs = 1.f, fs1 = 1.f;
+        if (kScaled) fs = feed_scale(p, it, id);
         for (int n = 0; n < it.nt; ++n) {
             const int tile = it.tile0 + n;
             const int id2 = n + 2 < it.nt ? feed_id<kTS>(p, it, tile + 2) : kNoBox;
-            if (kScaled) fs1 = feed_scales(p, it, id1);
+            if (kScaled) fs1 = feed_scale(p, it, id1);
             if (c >= stages &&
                 !warp_wait(KEYS ? bars.k_empty(ring.s) : bars.v_empty(ring.s), ring.ph ^ 1u, abort)) {
                 ok = false;
@@ -170,7 +170,8 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
                 if (a.status) atomicOr(a.status, KVC_DEV_OVERFLOW);
             }
             if (kScaled) feed_store(sc + c % kScaleRing, fs);
-            feed_copy<EB, kTS>(p, it, KEYS ? &p.tk : &p.tv, tile, id, base + ring.s * bytes, nb,
+            const uint32_t to = base + ring.s * bytes;
+            feed_copy<EB, kTS>(p, it, tile, id, to, KEYS ? nkb : 0, to, KEYS ? 0 : nvb,
                                KEYS ? bars.k_full(ring.s) : bars.v_full(ring.s));
             id = id1;
             id1 = id2;

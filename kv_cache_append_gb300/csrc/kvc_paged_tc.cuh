@@ -289,58 +289,63 @@ struct StageScales {
     float4 kv[kMaxBoxes];
 };
 
-// What a producer warp feeds a run's tiles from: box `lane` of a tile is hh slots
-// of one pool block. Block ids are read two tiles ahead and scales one, so no tile
-// waits for a look-up (with the look-ups in line, a tile took 1700 cycles before its
-// first copy went out, and the copies, not the arithmetic, bounded the kernels).
+// What a producer warp feeds a run's tiles from: box `lane % 16` of a tile is hh
+// slots of one pool block; lanes below 16 stand for its keys, the others for its values.
+// Block ids are read two tiles ahead and scales one, so no tile waits for a look-up,
+// and each lane issues its own box's copies (with the look-ups in line a tile took 1700
+// cycles before its first copy went out; copies issued in turn by one lane, with the
+// boxes' places handed round, took 1900 for four: either bounded the kernels).
 constexpr int kNoBox = -0x7fffffff;  // the box holds no visible slot: not read
+__device__ __forceinline__ int feed_box() { return threadIdx.x & 15; }
+__device__ __forceinline__ bool feed_values() { return (threadIdx.x & 16) != 0; }
 
 template <int TS>
 __device__ __forceinline__ int feed_id(const PagedTcParams& p, const PagedItem& it, int tile) {
-    const int lane = threadIdx.x & 31, slot = tile * TS + lane * p.hh;
-    if (lane * p.hh >= TS || slot + p.hh <= it.lo || slot > it.last) return kNoBox;
+    const int at = feed_box() * p.hh, slot = tile * TS + at;
+    if (at >= TS || slot + p.hh <= it.lo || slot > it.last) return kNoBox;
     return p.a.table[it.b * p.a.max_blocks + p.block_of(slot)];
 }
 __device__ __forceinline__ bool feed_bad(const PagedTcParams& p, int id) {
     return id != kNoBox && (id < 0 || id >= p.a.num_blocks);
 }
-// Key and value scale of a box (of one that is not read: anything finite).
-__device__ __forceinline__ float2 feed_scales(const PagedTcParams& p, const PagedItem& it, int id) {
-    if (id < 0 || id >= p.a.num_blocks) return make_float2(1.f, 1.f);
+// The box's key or value scale (of one that is not read: anything finite).
+__device__ __forceinline__ float feed_scale(const PagedTcParams& p, const PagedItem& it, int id) {
+    if (id < 0 || id >= p.a.num_blocks) return 1.f;
     const int64_t u = static_cast<int64_t>(id) * p.a.Hk + it.hk;
-    return make_float2(p.a.ks[u], p.a.vs[u]);
+    return (feed_values() ? p.a.vs : p.a.ks)[u];
 }
-__device__ __forceinline__ void feed_store(StageScales* sc, float2 s) {
-    const int lane = threadIdx.x & 31;
-    if (lane < kMaxBoxes) sc->kv[lane] = make_float4(s.x, s.y, __log2f(s.y), __fdividef(1.f, s.y));
-}
-// The copies of a tile, `nb` column blocks of 128 bytes for each box (block 0 in
-// place of a bad id); with `expect`, lane 0 first announces them and `extra` more.
-template <int EB, int TS>
-__device__ __forceinline__ void feed_copy(const PagedTcParams& p, const PagedItem& it,
-                                          const CUtensorMap* map, int tile, int id, uint32_t dst,
-                                          int nb, uint32_t full, bool expect = true, int extra = 0) {
-    constexpr int kElems = 128 / EB;  // elements of a column block
-    const int lane = threadIdx.x & 31;
-    const bool used = id != kNoBox;
-    // the boxes in use follow one another (and the vote orders the lanes' scales
-    // before the arrive that publishes the tile)
-    const uint32_t mask = __ballot_sync(0xffffffffu, used);
-    const int first = __ffs(mask) - 1, n = __popc(mask);
-    const int slot = tile * TS + lane * p.hh;
-    const int y = used ? slot - p.block_of(slot) * p.a.bs : 0;
-    const int z = used ? (feed_bad(p, id) ? 0 : id) * p.a.Hk + it.hk : 0;
-    __syncwarp();
-    if (expect && elect_one())
-        mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * (nb + extra) * p.hh * 128));
-    __syncwarp();
-    for (int c = first; c < first + n; ++c) {
-        const int yc = uniform(lane == c ? y : 0), zc = uniform(lane == c ? z : 0);
-        const uint32_t to = dst + static_cast<uint32_t>(c * p.hh * 128);
-        if (elect_one())
-            for (int k = 0; k < nb; ++k) tma_load_3d(to + k * TS * 128, map, kElems * k, yc, zc, full);
-        __syncwarp();
+__device__ __forceinline__ void feed_store(StageScales* sc, float s) {
+    float* kv = reinterpret_cast<float*>(&sc->kv[feed_box()]);
+    if (!feed_values()) {
+        kv[0] = s;
+    } else {
+        kv[1] = s;
+        kv[2] = __log2f(s);
+        kv[3] = __fdividef(1.f, s);
     }
+}
+// The copies of a tile's keys (nkb column blocks of 128 bytes for each box), values
+// (nvb) or both (block 0 in place of a bad id), announced on `full`.
+template <int EB, int TS>
+__device__ __forceinline__ void feed_copy(const PagedTcParams& p, const PagedItem& it, int tile, int id,
+                                          uint32_t sK, int nkb, uint32_t sV, int nvb, uint32_t full) {
+    constexpr int kElems = 128 / EB;  // elements of a column block
+    const bool values = feed_values();
+    const int nb = values ? nvb : nkb;
+    // (the vote also orders the lanes' scales before the arrive that publishes the tile)
+    const int n = __popc(__ballot_sync(0xffffffffu, id != kNoBox && !values));
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * (nkb + nvb) * p.hh * 128));
+    __syncwarp();
+    if (id != kNoBox) {
+        const int at = feed_box() * p.hh, slot = tile * TS + at;
+        const int y = slot - p.block_of(slot) * p.a.bs;
+        const int z = (feed_bad(p, id) ? 0 : id) * p.a.Hk + it.hk;
+        const uint32_t to = (values ? sV : sK) + static_cast<uint32_t>(at * 128);
+        const CUtensorMap* map = values ? &p.tv : &p.tk;
+        for (int k = 0; k < nb; ++k) tma_load_3d(to + k * TS * 128, map, kElems * k, y, z, full);
+    }
+    __syncwarp();
 }
 
 // A run's query rows into the swizzled operand layout, by one warp: rows w0, w0 +
