@@ -66,8 +66,10 @@ struct Bars {
     __device__ uint32_t o_done(int b) const { return base + 240u + 8u * b; }
     __device__ uint32_t meet(int g) const { return base + 256u + 8u * g; }
     __device__ uint32_t drained() const { return base + 272u; }
+    // the run is known (its query rows are not ready yet)
+    __device__ uint32_t item_known(int k) const { return base + 280u + 8u * k; }
 };
-constexpr int kTmemSlot = 280, kAbort = 284, kBad = 288 /* [4] */, kOdd = 304 /* [2] */;
+constexpr int kTmemSlot = 312, kAbort = 316, kBad = 320 /* [4] */, kOdd = 336 /* [2] */;
 // from 512: PagedStart (read before the first tile is loaded), then the stages'
 // StageScales; then the items and their rows' data
 
@@ -140,9 +142,11 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
             !warp_wait(bars.item_empty(kb), static_cast<uint32_t>((k / p.ni - 1) & 1), abort))
             return;
         if (!more) {
-            if (lane == 0) items[kb].flags = kItemDone;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);
+            if (lane == 0) {
+                items[kb].flags = kItemDone;
+                mbar_arrive(bars.item_known(kb), 1u);
+                mbar_arrive(bars.item_full(kb), 1u);
+            }
             return;
         }
         unsigned char* sq = smem + p.off_q + kb * p.q_bytes;
@@ -151,6 +155,7 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
         if (lane == 0) {
             items[kb] = it;
             *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 0;
+            mbar_arrive(bars.item_known(kb), 1u);
         }
         {
             const int r = it.r0 + lane;
@@ -181,7 +186,7 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
-        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (!warp_wait(bars.item_known(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
         const PagedItem it = items[kb];
         if (it.flags & kItemDone) break;
         int id = feed_id<kTS>(p, it, it.tile0);
@@ -645,6 +650,7 @@ __global__ void __launch_bounds__(Roles<SG>::threads, EB == 1 && NR <= 16 ? 2 : 
             mbar_init(bars.empty(s), 1u);
         }
         for (int k = 0; k < p.ni; ++k) {
+            mbar_init(bars.item_known(k), 1u);
             mbar_init(bars.item_full(k), 1u);
             mbar_init(bars.item_empty(k), 3u + R::soft);  // producer, both issuers, softmax warps
         }
@@ -658,6 +664,8 @@ __global__ void __launch_bounds__(Roles<SG>::threads, EB == 1 && NR <= 16 ? 2 : 
         mbar_init(bars.drained(), 2u);
         *abort = 0;
         fence_mbar_init();
+        prefetch_map(&p.tk);
+        prefetch_map(&p.tv);
     }
     // weights of rows past the unit's stay zero: clear the buffers once
     for (int i = threadIdx.x; i < S::npt * S::pbytes / 16; i += kThreads)

@@ -59,9 +59,11 @@ struct Bars {
     __device__ uint32_t meet() const { return base + 456u; }
     __device__ uint32_t o_free() const { return base + 464u; }
     __device__ uint32_t drained() const { return base + 472u; }
+    // the run is known (its query rows are not ready yet)
+    __device__ uint32_t item_known(int k) const { return base + 480u + 8u * k; }
 };
-constexpr int kTmemSlot = 480, kAbort = 484, kBad = 488 /* [2] */, kOdd = 496 /* [2] */;
-constexpr int kStart = 512, kItems = 896;
+constexpr int kTmemSlot = 496, kAbort = 500, kBad = 504 /* [2] */, kOdd = 512 /* [2] */;
+constexpr int kStart = 576, kItems = 896;
 // exchanged between the groups, for even and odd runs: a row's reference [2][128],
 // each group's sum and the reference it is measured by [2][3][128]
 constexpr int kXr = 1024, kXl = 2048;
@@ -112,7 +114,10 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
             !warp_wait(bars.item_empty(kb), static_cast<uint32_t>((k / p.ni - 1) & 1), abort))
             return;
         if (!more) {
-            if (qw == 0 && lane == 0) items[kb].flags = kItemDone;
+            if (qw == 0 && lane == 0) {
+                items[kb].flags = kItemDone;
+                mbar_arrive(bars.item_known(kb), 1u);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);
             return;
@@ -122,6 +127,7 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
         if (qw == 0 && lane == 0) {
             items[kb] = it;
             *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 0;
+            mbar_arrive(bars.item_known(kb), 1u);
         }
         prepare_rows<T, EB, kRows>(p, it, sq, nkb, kBlk, qw, 4, lane, EB == 1 ? mul : nullptr);
         fence_async_shared();  // the query rows, for the tensor cores
@@ -148,7 +154,7 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int kb = k % p.ni;
-        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
+        if (!warp_wait(bars.item_known(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) break;
         const PagedItem it = items[kb];
         if (it.flags & kItemDone) break;
         constexpr bool kScaled = EB == 1 && KEYS;
@@ -645,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             mbar_init(bars.v_empty(s), 1u);
         }
         for (int k = 0; k < 2; ++k) {
+            mbar_init(bars.item_known(k), 1u);
             mbar_init(bars.item_full(k), 4u);         // the query warps
             mbar_init(bars.item_empty(k), 4u + kSoft);  // producers, issuers, softmax warps
         }
@@ -662,6 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         *reinterpret_cast<volatile int*>(smem + kOdd) = 0;
         *reinterpret_cast<volatile int*>(smem + kOdd + 4) = 0;
         fence_mbar_init();
+        prefetch_map(&p.tk);
+        prefetch_map(&p.tv);
     }
     if (warp == kSWarp) {
         tmem_alloc(smem_addr(smem + kTmemSlot), 512);

@@ -60,6 +60,10 @@ __device__ __forceinline__ uint32_t mma_idesc_f8(int M, int N, bool a_e5m2, bool
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // One lane of a converged warp. The issuing warps run as a whole, on values that
 // are the same in all lanes, and only the tensor-core instructions stand behind
 // this: their operands are then uniform registers. (Issued by a lone thread of a
