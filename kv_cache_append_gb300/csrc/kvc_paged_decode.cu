@@ -163,7 +163,7 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
             rd->lim[lane] = live ? it.K - it.S + r / a.G : -1;
             rd->slope[lane] = live && a.slopes ? a.slopes[it.hk * a.G + r % a.G] * kLog2e : 0.f;
         }
-        prepare_rows<T, EB, DN>(p, it, sq, nkb, S::nblk, 0, 1, lane, rd->mul);
+        prepare_rows<T, EB, DN, 32>(p, it, sq, nkb, S::nblk, lane, rd->mul);
         fence_async_shared();  // the query rows, for the tensor cores
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);

@@ -129,7 +129,7 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
             *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 0;
             mbar_arrive(bars.item_known(kb), 1u);
         }
-        prepare_rows<T, EB, kRows>(p, it, sq, nkb, kBlk, qw, 4, lane, EB == 1 ? mul : nullptr);
+        prepare_rows<T, EB, kRows, 128>(p, it, sq, nkb, kBlk, 32 * qw + lane, EB == 1 ? mul : nullptr);
         fence_async_shared();  // the query rows, for the tensor cores
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.item_full(kb), 1u);

@@ -167,7 +167,10 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
         st->total = total;
         st->per = per;
     }
-    if (at >= cur && at < cur + mine) {
+    if (per_thread == 1 && at >= cur && at < cur + mine) {
+        st->b = static_cast<int>(b0);
+        st->off = at - cur;
+    } else if (at >= cur && at < cur + mine) {
         for (int64_t b = b0; b < b1; ++b) {
             const long long n = paged_seq_tiles<TS>(p, b, &invalid);
             if (at < cur + n) {
@@ -352,100 +355,86 @@ __device__ __forceinline__ void feed_copy(const PagedTcParams& p, const PagedIte
     __syncwarp();
 }
 
-// A run's query rows into the swizzled operand layout, by one warp: rows w0, w0 +
-// step, ... of ROWS (rows past the unit's are zero). 8-bit products: hi parts, then
-// lo parts, both e4m3, of the row times the power of two that takes its largest
-// element into [2^7, 2^8); mul[r] is the score scale over that power. Several rows'
-// loads are under way at a time: one by one, the 32 rows of a warp took 20 us.
-template <typename T, int EB, int ROWS>
+// A run's query rows into the swizzled operand layout, by THREADS threads, one or
+// two for a row (rows past the unit's are zero). 8-bit products: hi parts, then lo
+// parts, both e4m3, of the row times the power of two that takes its largest element
+// into [2^7, 2^8); mul[r] is the score scale over that power. (A warp for a row at a time
+// needed a reduction and a division for each: 45 us for 128 rows of 192.)
+template <typename T, int EB, int ROWS, int THREADS>
 __device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const PagedItem& it,
-                                             unsigned char* sq, int nkb, int blk, int w0, int step,
-                                             int lane, float* mul) {
+                                             unsigned char* sq, int nkb, int blk, int tid, float* mul) {
+    constexpr int kPerRow = THREADS / ROWS;
+    static_assert(kPerRow == 1 || (kPerRow == 2 && THREADS == 32), "one thread for a row, or two lanes");
     const PagedAttendParams& a = p.a;
+    const int r = tid % ROWS, part = tid / ROWS;
     const int R = min(p.RG, it.S * a.G - it.r0);
-    const T* base = static_cast<const T*>(a.q) + static_cast<int64_t>(it.hk) * a.G * a.q_head;
-    auto row_ptr = [&](int r) {
-        const int rr = it.r0 + r, t = rr / a.G;
-        return base + (it.q0 + t) * a.q_tok + (rr - t * a.G) * a.q_head;
-    };
+    const bool live = r < R;
+    const int rr = it.r0 + (live ? r : 0), t = rr / a.G;
+    const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(it.q0 + t) * a.q_tok +
+                 (static_cast<int64_t>(it.hk) * a.G + (rr - t * a.G)) * a.q_head;
+    const int nch = nkb * 8;  // 16-byte chunks of a row in shared memory
+    unsigned char* dst = sq + r * 128;
     if (EB == 2) {
-        // 16-byte chunks of the rows in one list
-        const int cpr = nkb * 8, n = ROWS / step * cpr;
-        constexpr int kAhead = 4;
-        for (int i0 = lane; i0 < n; i0 += 32 * kAhead) {
-            uint4 v[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + 32 * u, r = w0 + i / cpr * step, c = i % cpr;
-                v[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (i < n && r < R && c * 8 < a.D)
-                    v[u] = *reinterpret_cast<const uint4*>(row_ptr(r) + c * 8);
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + 32 * u, r = w0 + i / cpr * step, c = i % cpr;
-                if (i < n)
-                    *reinterpret_cast<uint4*>(sq + (c >> 3) * blk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                        v[u];
-            }
+#pragma unroll 4
+        for (int c = part; c < nch; c += kPerRow) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (live && c * 8 < a.D) v = *reinterpret_cast<const uint4*>(q + c * 8);
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * blk + (((c & 7) ^ (r & 7)) << 4)) = v;
         }
-        if (mul)
-            for (int r = w0 + lane * step; r < ROWS; r += 32 * step) mul[r] = a.scale;
+        if (mul && part == 0) mul[r] = a.scale;
         return;
     }
-    constexpr int kAhead = 4;  // rows
-    for (int r0 = w0; r0 < ROWS; r0 += kAhead * step) {
-        uint2 v[kAhead][2];  // lane: elements 4 lane .. of each 128
+    auto word2 = [&](int d) {  // four elements
+        return live && d < a.D ? *reinterpret_cast<const uint2*>(q + d) : make_uint2(0u, 0u);
+    };
+    constexpr uint32_t kInf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+    uint32_t big = 0;  // the largest finite magnitude, as its 16 bits
+#pragma unroll 2
+    for (int c = part; c < nch; c += kPerRow) {
+        uint2 v[4];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int r = r0 + u * step;
+        for (int e = 0; e < 4; ++e) v[e] = word2(c * 16 + e * 4);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int d = c * 128 + lane * 4;
-                v[u][c] = make_uint2(0u, 0u);
-                if (r < R && d < a.D) v[u][c] = *reinterpret_cast<const uint2*>(row_ptr(r) + d);
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w[2] = {v[e].x, v[e].y};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t lo = w[h] & 0x7fffu, hi = (w[h] >> 16) & 0x7fffu;
+                if (lo < kInf) big = max(big, lo);
+                if (hi < kInf) big = max(big, hi);
             }
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int r = r0 + u * step;
-            if (r >= ROWS) break;
-            float x[2][4], big = 0.f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const T* h = reinterpret_cast<const T*>(&v[u][c]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[c][e] = Storage<T>::to_float(h[e]);
-                    if (fabsf(x[c][e]) < INFINITY)
-                        big = fmaxf(big, fabsf(x[c][e]));
-                    else
-                        x[c][e] = __uint_as_float(0x7fffffffu);  // no 8-bit infinity: NaN
-                }
-            }
-            big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-            int e2 = 7 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
-            e2 = max(-120, min(120, e2));
-            const float f = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (c >= nkb) break;
-                uint32_t hi = 0, lo = 0;
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float y0 = x[c][e] * f, y1 = x[c][e + 1] * f;
-                    const uint32_t h2 = to_eight2<false>(y0, y1);
-                    const float2 hf = from_eight2<false>(h2);
-                    hi |= h2 << (8 * e);
-                    lo |= to_eight2<false>(y0 - hf.x, y1 - hf.y) << (8 * e);
-                }
-                const int o = c * blk + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                *reinterpret_cast<uint32_t*>(sq + o) = hi;
-                *reinterpret_cast<uint32_t*>(sq + nkb * blk + o) = lo;
-            }
-            if (lane == 0) mul[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
         }
     }
+    if (kPerRow == 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, 16));
+    const unsigned short raw = static_cast<unsigned short>(big);
+    const float bigf = Storage<T>::to_float(*reinterpret_cast<const T*>(&raw));
+    int e2 = 7 - (static_cast<int>(__float_as_uint(bigf) >> 23) - 127);
+    e2 = max(-120, min(120, e2));
+    const float f = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+#pragma unroll 1
+    for (int c = part; c < nch; c += kPerRow) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint2 v = word2(c * 16 + e * 4);
+            const T* x = reinterpret_cast<const T*>(&v);
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[k] = Storage<T>::to_float(x[k]) * f;
+                if (!(fabsf(y[k]) < INFINITY)) y[k] = __uint_as_float(0x7fffffffu);  // no infinity: NaN
+            }
+            const uint32_t h0 = to_eight2<false>(y[0], y[1]), h1 = to_eight2<false>(y[2], y[3]);
+            const float2 f0 = from_eight2<false>(h0), f1 = from_eight2<false>(h1);
+            hi[e] = h0 | (h1 << 16);
+            lo[e] = to_eight2<false>(y[0] - f0.x, y[1] - f0.y) |
+                    (to_eight2<false>(y[2] - f1.x, y[3] - f1.y) << 16);
+        }
+        unsigned char* o = dst + (c >> 3) * blk + (((c & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(o + nkb * blk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    if (part == 0) mul[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
 }
 
 // Four weights as three e5m2 parts each (a word of four codes per part). e5m2
