@@ -229,7 +229,6 @@ struct PagedTcParams {
     int hh;            // slots of a box: the largest power of two up to 128 dividing block_size
     int ns, ni;        // stages (rows kernel: of keys), item and query buffers
     int nv;            // rows kernel: stages of values
-    int off_half;      // rows kernel, 8-bit pools: two value tiles in fp16
     int off_item, off_q, off_x, off_p, off_stage;  // shared memory
     int q_bytes, stage_bytes;
     float* part_ml;    // [2 ctas][RG][2]

@@ -129,12 +129,10 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         while (d.block_size % p.hh != 0) p.hh /= 2;
         p.off_q = es == 1 ? 12288 : 8192;  // scales of 16 tiles, or none
         p.q_bytes = static_cast<int>(parts * kb + (es == 1 ? 1024 : 0));
-        const int64_t half = es == 1 ? 2 * ((d.Dv * 2 + 127) / 128) * 128 * 128 : 0;
         // the next run's query rows are prepared ahead where that leaves three tiles
-        // (two and the converted ones)
-        int64_t room = kSmemBlock - p.off_q - half - 2 * p.q_bytes;
-        p.ni = room >= (es == 1 ? 2 : 3) * (kb + vb) ? 2 : 1;
-        room = kSmemBlock - p.off_q - half - p.ni * p.q_bytes;
+        int64_t room = kSmemBlock - p.off_q - 2 * p.q_bytes;
+        p.ni = room >= 3 * (kb + vb) ? 2 : 1;
+        room = kSmemBlock - p.off_q - p.ni * p.q_bytes;
         const int64_t pairs = std::min<int64_t>(8, room / (kb + vb));
         if (pairs < 1) return t;
         room -= pairs * (kb + vb);
@@ -142,8 +140,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         if (p.ns > pairs) room -= kb;
         p.nv = static_cast<int>(pairs < 8 && room >= vb ? pairs + 1 : pairs);
         if (p.ns < 2) return t;
-        p.off_half = p.off_q + p.ni * p.q_bytes;
-        p.off_stage = static_cast<int>(p.off_half + half);
+        p.off_stage = p.off_q + p.ni * p.q_bytes;
         t.smem = static_cast<size_t>(p.off_stage + p.ns * kb + p.nv * vb);
         p.ctas = static_cast<int>(kPlanSms);
         tc_workspace(d, &t);

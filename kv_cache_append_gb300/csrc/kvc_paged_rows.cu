@@ -7,14 +7,11 @@
 //   S  = Q K^T    (A = query rows, B = K tile, both from shared memory)
 //   O += P V      (A = P from tensor memory, B = V tile read N-major)
 //
-// With 8-bit pools S takes the key tiles as they lie in memory, the query rows as
-// two e4m3 parts (split, scales and references as in kvc_paged_decode.cu), at twice the
-// 16-bit rate: the time of one 16-bit product, with half the memory traffic. The value
-// tiles are turned into fp16 (which holds every value of both formats) by four warps of
-// their own, 500 instructions a tile, and the weights rounded to fp16 once: three
-// e5m2 parts of every weight instead were 3 more instructions an element for the
-// softmax warps, and 2.0 instead of 3.2 thousand cycles a tile are what is left
-// without (prompts of 128-wide heads, 1.9 GHz).
+// With 8-bit pools both products take the tiles as they lie in memory, the
+// query rows as two e4m3 parts and the weights as three e5m2 parts (splits, scales
+// and references as in kvc_paged_decode.cu): five products at twice the 16-bit
+// rate against four halves, so the tensor-core time is 5/4 of 16-bit tiles', with
+// half the memory traffic and no conversion of the cache.
 //
 // The softmax, not the products, is the longer part of a tile, and a tile's chain
 // (S, softmax, P V, the next S into the same columns) is longer still: three groups
@@ -23,13 +20,13 @@
 // so a row has one reference: tile n's warp reads what tile n - 1's warp of the
 // same rows left before it makes its weights (a decision comes after the first of a
 // tile's two passes, and raising is rare), and each group measures its sum by the
-// reference it last saw. P overwrites its S in place: the weights of 32 slots take 16
-// columns, behind the 32 score columns that are read next.
+// reference it last saw. P overwrites its S in place: the weights of 32 slots take 24
+// columns (16 of 16-bit weights), behind the 32 score columns that are read next.
 //
 // Tensor memory: S of the groups at columns 0, 128 and 256, O at 384. Warps: 12
 // softmax, an S issuer, a P.V issuer, a producer of key tiles and one of value tiles,
-// 4 that schedule the block's runs (kvc_paged_tc.cuh) and prepare the next run's
-// query rows, and with 8-bit pools 4 that convert value tiles.
+// and 4 that schedule the block's runs (kvc_paged_tc.cuh) and prepare the next
+// run's query rows.
 #include <algorithm>
 #include <type_traits>
 
@@ -42,9 +39,7 @@ constexpr int kTS = 128, kRows = 128;
 constexpr int kGroups = 3;                 // of 4 softmax warps, tiles in turn
 constexpr int kSoft = 4 * kGroups;
 constexpr int kSWarp = 12, kPvWarp = 13, kKWarp = 14, kVWarp = 15, kQWarp = 16;  // 16..19: query rows
-constexpr int kCvtWarp = 20;  // 20..23, 8-bit pools: value tiles to fp16
-template <int EB>
-struct Threads { static constexpr int v = (EB == 1 ? 24 : 20) * 32; };
+constexpr int kThreads = 20 * 32;
 constexpr uint32_t kColS = 0, kColO = 384;  // S buffers of the three groups, O
 
 struct Bars {
@@ -66,9 +61,6 @@ struct Bars {
     __device__ uint32_t drained() const { return base + 472u; }
     // the run is known (its query rows are not ready yet)
     __device__ uint32_t item_known(int k) const { return base + 480u + 8u * k; }
-    // 8-bit pools: the fp16 value tiles
-    __device__ uint32_t h_full(int k) const { return base + 528u + 8u * k; }
-    __device__ uint32_t h_empty(int k) const { return base + 544u + 8u * k; }
 };
 constexpr int kTmemSlot = 496, kAbort = 500, kBad = 504 /* [2] */, kOdd = 512 /* [2] */;
 constexpr int kStart = 576, kItems = 896;
@@ -88,6 +80,16 @@ struct Turn {
         }
     }
 };
+
+__device__ __forceinline__ void tc_mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
 
 // 4 warps: lane 0 of the first walks the runs; all split the rows of the run.
 template <typename T, int EB>
@@ -265,12 +267,11 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
                           uint32_t tmem) {
     const PagedAttendParams& a = p.a;
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + kItems);
-    // the 16-bit value tiles: the ring itself, or the converted ones
-    const int nb = (a.Dv * 2 + 127) / 128, stages = EB == 1 ? 2 : p.nv;
-    const uint32_t sV0 = smem_addr(smem) +
-                         (EB == 1 ? p.off_half : p.off_stage + p.ns * ((a.D * 2 + 127) / 128) * kTS * 128);
+    const int nkb = (a.D * EB + 127) / 128, nvb = (a.Dv * EB + 127) / 128;
+    const uint32_t sV0 = smem_addr(smem + p.off_stage) + p.ns * nkb * kTS * 128;
     const int N = (a.Dv + 15) / 16 * 16;
-    const uint32_t idesc = mma_idesc_f16(kRows, N, EB == 2 && std::is_same<T, __nv_bfloat16>::value, true);
+    const uint32_t idesc = EB == 1 ? mma_idesc_f8(kRows, N, true, a.e5m2, false, true)
+                                   : mma_idesc_f16(kRows, N, std::is_same<T, __nv_bfloat16>::value, true);
     Ring vr;
     Turn turn;
     bool ok = true;
@@ -283,23 +284,33 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
         if (k > 0 && !warp_wait(bars.o_free(), static_cast<uint32_t>((k - 1) & 1), abort)) break;
         for (int n = 0; n < nt; ++n) {
             const int g = turn.g;
-            if (!warp_wait(EB == 1 ? bars.h_full(vr.s) : bars.v_full(vr.s), vr.ph, abort) ||
+            if (!warp_wait(bars.v_full(vr.s), vr.ph, abort) ||
                 !warp_wait(bars.p_ready(g), turn.ph, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
+            const uint32_t sV = sV0 + vr.s * nvb * kTS * 128;
             const uint32_t tP = tmem + kColS + 128 * g, tO = tmem + kColO;
-            const uint64_t dv = smem_desc_sw128(sV0 + vr.s * nb * kTS * 128, kTS * 128, 1024);
+            const uint64_t dv = smem_desc_sw128(sV, kTS * 128, 1024);
             if (elect_one()) {
+                if (EB == 1) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)  // 16 slots per step
-                    tc_mma_ts(tO, tP + 8 * i, dv + i * (16 * 128 / 16), idesc, (n | i) != 0);
+                    for (int i = 0; i < 4; ++i)  // 32 slots per step
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+                            tc_mma_f8_ts(tO, tP + 24 * i + 8 * part,
+                                         dv + i * (32 * 128 / 16), idesc, (n | i | part) != 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)  // 16 slots per step
+                        tc_mma_ts(tO, tP + 8 * i, dv + i * (16 * 128 / 16), idesc, (n | i) != 0);
+                }
                 tc_commit(bars.o_done(g));
-                tc_commit(EB == 1 ? bars.h_empty(vr.s) : bars.v_empty(vr.s));
+                tc_commit(bars.v_empty(vr.s));
             }
             __syncwarp();
-            vr.next(stages);
+            vr.next(p.nv);
             turn.next();
         }
         if (ok && elect_one()) mbar_arrive(bars.item_empty(kb), 1u);
@@ -309,82 +320,6 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
     __syncwarp();
     volatile int never = 0;
     warp_wait(bars.drained(), 0u, &never);
-}
-
-// A slot's value row that no row of the unit sees, or some see and others do not.
-struct SlotSeen {
-    bool some, all;
-};
-__device__ __forceinline__ SlotSeen slot_seen(const PagedAttendParams& a, const PagedItem& it, int j) {
-    SlotSeen s;
-    s.some = j <= it.last && j >= it.lo;
-    s.all = j <= it.first && (a.window == 0 || j > it.last - a.window);
-    return s;
-}
-
-// 8-bit pools, 4 warps: thread r turns slot r's value row into fp16 (exact), cleared
-// where no query row sees the slot, and of infinities and NaN where some do not.
-__device__ void convert_warps(const PagedTcParams& p, unsigned char* smem, Bars bars,
-                              volatile int* abort) {
-    const PagedAttendParams& a = p.a;
-    const int lane = threadIdx.x & 31, r = threadIdx.x & 127;
-    const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + kItems);
-    const int nkb = (a.D + 127) / 128, nhb = (a.Dv * 2 + 127) / 128;
-    const unsigned char* raw0 = smem + p.off_stage + p.ns * nkb * kTS * 128 + r * 128;
-    unsigned char* half0 = smem + p.off_half + r * 128;
-    int c = 0;
-    Ring vr, hr;
-    for (int k = 0;; ++k) {
-        const int kb = k % p.ni;
-        if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) return;
-        const PagedItem it = items[kb];
-        if (it.flags & kItemDone) return;
-        volatile int* odd = reinterpret_cast<volatile int*>(smem + kOdd + 4 * (k & 1));
-        for (int n = 0; n < it.nt; ++n, ++c) {
-            if (!warp_wait(bars.v_full(vr.s), vr.ph, abort) ||
-                (c >= 2 && !warp_wait(bars.h_empty(hr.s), hr.ph ^ 1u, abort)))
-                return;
-            const unsigned char* raw = raw0 + vr.s * kTS * 128;
-            unsigned char* out = half0 + hr.s * nhb * kTS * 128;
-            const SlotSeen seen = slot_seen(a, it, (it.tile0 + n) * kTS + r);
-#pragma unroll 2
-            for (int q = 0; q < nhb * 4; ++q) {  // 16 values at a time
-                const uint4 w = *reinterpret_cast<const uint4*>(raw + ((q ^ (r & 7)) << 4));
-                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                uint32_t h[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_fp8x2_storage_t b0 = static_cast<__nv_fp8x2_storage_t>(in[e] & 0xffffu);
-                    const __nv_fp8x2_storage_t b1 = static_cast<__nv_fp8x2_storage_t>(in[e] >> 16);
-                    const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2(b0, a.e5m2 ? __NV_E5M2 : __NV_E4M3);
-                    const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2(b1, a.e5m2 ? __NV_E5M2 : __NV_E4M3);
-                    h[2 * e] = h0.x | (static_cast<uint32_t>(h0.y) << 16);
-                    h[2 * e + 1] = h1.x | (static_cast<uint32_t>(h1.y) << 16);
-                }
-                if (!seen.all) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t u = seen.some ? clear_odd<2, __half>(h[e], false) : 0u;
-                        if (seen.some && u != h[e]) *odd = k + 1;
-                        h[e] = u;
-                    }
-                }
-                unsigned char* o = out + (q >> 2) * kTS * 128;
-                const int ch = (2 * q) & 7;
-                *reinterpret_cast<uint4*>(o + ((ch ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(o + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-            fence_async_shared();  // for the tensor cores
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bars.v_empty(vr.s), 1u);
-                mbar_arrive(bars.h_full(hr.s), 1u);
-            }
-            vr.next(p.nv);
-            hr.next(2);
-        }
-        if (lane == 0) mbar_arrive(bars.item_empty(kb), 1u);
-    }
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -546,7 +481,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 float s[32];
                 tmem_ld32(tS + 32 * q, s);
                 if (!MOD && edge) hide_columns(s, lim - j0 - 32 * q, low - j0 - 32 * q);
-                uint32_t w[16];
+                uint32_t w[EB == 1 ? 24 : 16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     float f = MOD ? 1.f : mul, lv = off, ivs = 1.f;
@@ -568,28 +503,39 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                         x[i + 1] = fast_exp2(v.y);
                         sum = add2(sum, make_float2(x[i], x[i + 1]));
                     }
-                    if (EB == 1) l = fmaf(sum.x + sum.y, ivs, l);
-                    using P = std::conditional_t<EB == 1, __half, T>;
+                    if (EB == 1) {
+                        l = fmaf(sum.x + sum.y, ivs, l);
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack2<P>(x[i], x[i + 1]);
+                        for (int i = 0; i < 8; i += 4) {
+                            uint32_t part[3];
+                            split_weights(x[i], x[i + 1], x[i + 2], x[i + 3], part);
+#pragma unroll
+                            for (int k2 = 0; k2 < 3; ++k2) w[8 * k2 + (e + i) / 4] = part[k2];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack2<T>(x[i], x[i + 1]);
+                    }
                 }
+                constexpr int kWords = EB == 1 ? 24 : 16;
 #pragma unroll
-                for (int i = 0; i < 16; i += 8) tmem_st8_async(tS + 16 * q + i, w + i);
+                for (int i = 0; i < kWords; i += 8) tmem_st8_async(tS + kWords * q + i, w + i);
             }
             if (EB == 2) l += sum.x + sum.y;
             tmem_wait_st();
-            if (EB == 2 && edge) {  // thread r looks after slot r's value row
+            if (edge) {  // thread r looks after slot r's value row
                 if (!warp_wait(bars.v_full(stage), sph, abort)) return;
                 const int j = j0 + r;
                 unsigned char* vrow = sV0 + stage * nvb * kTS * 128 + r * 128;
-                const SlotSeen seen = slot_seen(a, it, j);
-                if (!seen.some) {
+                const bool some = j <= it.last && j >= it.lo;
+                const bool all = j <= it.first && (a.window == 0 || j > it.last - a.window);
+                if (!some) {
                     for (int b = 0; b < nvb; ++b)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             *reinterpret_cast<uint4*>(vrow + b * kTS * 128 + i * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
-                } else if (!seen.all) {
+                } else if (!all) {
                     for (int b = 0; b < nvb; ++b)
 #pragma unroll 4
                         for (int i = 0; i < 32; ++i) {
@@ -689,8 +635,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
 }
 
 template <typename T, int EB, bool MOD>
-__global__ void __launch_bounds__(Threads<EB>::v, 1) paged_rows_kernel(const __grid_constant__ PagedTcParams p) {
-    constexpr int kThreads = Threads<EB>::v;
+__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_constant__ PagedTcParams p) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const Bars bars{smem_addr(smem)};
     volatile int* abort = reinterpret_cast<volatile int*>(smem + kAbort);
@@ -703,15 +648,12 @@ __global__ void __launch_bounds__(Threads<EB>::v, 1) paged_rows_kernel(const __g
         }
         for (int s = 0; s < p.nv; ++s) {
             mbar_init(bars.v_full(s), 1u);
-            mbar_init(bars.v_empty(s), EB == 1 ? 4u : 1u);  // the converting warps, or the product
+            mbar_init(bars.v_empty(s), 1u);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(bars.item_known(k), 1u);
             mbar_init(bars.item_full(k), 4u);         // the query warps
-            // producers, issuers, softmax and converting warps
-            mbar_init(bars.item_empty(k), 4u + kSoft + (EB == 1 ? 4u : 0u));
-            mbar_init(bars.h_full(k), 4u);
-            mbar_init(bars.h_empty(k), 1u);
+            mbar_init(bars.item_empty(k), 4u + kSoft);  // producers, issuers, softmax warps
         }
         for (int g = 0; g < kGroups; ++g) {
             mbar_init(bars.s_ready(g), 1u);
@@ -740,19 +682,13 @@ __global__ void __launch_bounds__(Threads<EB>::v, 1) paged_rows_kernel(const __g
     const uint32_t tmem = uniform(*reinterpret_cast<volatile int*>(smem + kTmemSlot));
     launch_dependents();
 
-    // registers: of the launch's 24 x 80 (20 x 96), 12 softmax warps take 112 (120) a
-    // thread, the others 48 (56)
+    // 120 registers for a softmax thread, 56 for the others: 12 warps x 120 + 8 x 56 <=
+    // the launch's 20 x 96
     if (warp < kSoft) {
-        if (EB == 1)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-        else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         softmax_warps<T, EB, MOD>(p, smem, bars, abort, tmem);
     } else {
-        if (EB == 1)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kSWarp) {
             s_issuer<T, EB>(p, smem, bars, abort, tmem);
         } else if (warp == kPvWarp) {
@@ -761,8 +697,6 @@ __global__ void __launch_bounds__(Threads<EB>::v, 1) paged_rows_kernel(const __g
             producer_warp<EB, true>(p, smem, bars, abort);
         } else if (warp == kVWarp) {
             producer_warp<EB, false>(p, smem, bars, abort);
-        } else if (EB == 1 && warp >= kCvtWarp) {
-            convert_warps(p, smem, bars, abort);
         } else if (warp >= kQWarp) {
             query_warps<T, EB>(p, smem, bars, st, abort);
         }
@@ -782,7 +716,7 @@ cudaError_t launch_t(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
     static SmemLimit limit;
     cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern));
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(p.ctas), Threads<EB>::v, smem, stream>>>(p);
+    kern<<<static_cast<unsigned>(p.ctas), kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 template <typename T, int EB>

@@ -95,15 +95,15 @@ def dense(pool, scale, table, b, K):
 # the products see them, beyond fp32 arithmetic.
 #   cores: fp32 throughout.
 #   tensor cores, 8-bit pools: a query element is the sum of two e4m3 values (each
-#   off by at most 2^-4 of what it rounds: 2^-8), a weight its fp16 rounding (2^-11),
-#   in the decode kernel as three e5m2 values, two cut to 3 bits and one rounded: 2^-9
-#   more, or 2^-25 of the largest.
+#   off by at most 2^-4 of what it rounds: 2^-8), a weight the sum of three e5m2
+#   values of its fp16 rounding, two cut to 3 bits and one rounded: 2^-9 + 2^-11, or 2^-25
+#   of the largest.
 #   tensor cores, pools of the inputs' type: the query exact, a weight rounded to the type.
 def operand_errors(path, q_dtype, eight):
     if path == "cores":
         return 0.0, 0.0
     if eight:
-        return 2.0 ** -8, 2.0 ** -8 if path == "decode" else 2.0 ** -11
+        return 2.0 ** -8, 2.0 ** -8
     return 0.0, UNIT[q_dtype]
 
 
