@@ -130,12 +130,12 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
     const int nkb = (a.D * EB + 127) / 128;
     PagedWalk<kTS> w;
     w.start(p, st);
-    const long long unit0 = w.at - w.tt;
+    const int before = w.tt;
     PagedItem it;
     int unit_tiles = 0;
     bool more = w.next(p, it, unit_tiles);
     if (lane == 0)
-        paged_record(p, more && !(it.flags & kItemBegins) ? &it : nullptr, unit0, unit_tiles, w.per);
+        paged_record(p, more && !(it.flags & kItemBegins) ? &it : nullptr, before, unit_tiles, w.per);
     for (int k = 0;; ++k) {
         const int kb = k % p.ni;
         if (k >= p.ni &&
@@ -524,26 +524,9 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             if (edge && g == 0) {
                 unsigned char* vrow = smem + p.off_stage + static_cast<int64_t>(ring.s) * p.stage_bytes +
                                       nkb * kTS * 128 + t * 128;
-                const bool some = j <= it.last && j >= it.lo;
-                const bool all = j <= it.first && (a.window == 0 || j > it.last - a.window);
-                if (!some) {
-                    for (int b = 0; b < nvb; ++b)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4*>(vrow + b * kTS * 128 + i * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                } else if (!all) {
-                    for (int b = 0; b < nvb; ++b)
-                        for (int i = 0; i < 32; ++i) {
-                            uint32_t* w = reinterpret_cast<uint32_t*>(vrow + b * kTS * 128) +
-                                          ((i + lane) & 31);
-                            const uint32_t v = *w, u = clear_odd<EB, T>(v, a.e5m2);
-                            if (u != v) {
-                                *w = u;
-                                *odd = 1;
-                            }
-                        }
-                }
+                const bool some_see = j <= it.last && j >= it.lo;
+                const bool all_see = j <= it.first && (a.window == 0 || j > it.last - a.window);
+                if (!all_see && clean_value_row<EB, T>(vrow, nvb, kTS * 128, some_see, a.e5m2)) *odd = 1;
             }
             if (rescale && n > 0) {
                 // O^T is at rest: the previous product has finished, this tile's

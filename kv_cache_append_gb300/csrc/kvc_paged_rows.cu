@@ -102,12 +102,12 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
     constexpr int kBlk = kRows * 128;
     PagedWalk<kTS> w;  // each warp walks alike
     w.start(p, st);
-    const long long unit0 = w.at - w.tt;
+    const int before = w.tt;
     PagedItem it;
     int unit_tiles = 0;
     bool more = w.next(p, it, unit_tiles);
     if (qw == 0 && lane == 0)
-        paged_record(p, more && !(it.flags & kItemBegins) ? &it : nullptr, unit0, unit_tiles, w.per);
+        paged_record(p, more && !(it.flags & kItemBegins) ? &it : nullptr, before, unit_tiles, w.per);
     for (int k = 0;; ++k) {
         const int kb = k % p.ni;
         if (k >= p.ni &&
@@ -335,7 +335,8 @@ __device__ __forceinline__ void hide_columns(float (&s)[32], int hi, int lo) {
         if (i > hi || i <= lo) s[i] = -INFINITY;
 }
 
-template <typename T, int EB, bool MOD>
+// WIDE (8-bit pools): the boxes have 32 slots or more, so 32 columns share their scales.
+template <typename T, int EB, bool MOD, bool WIDE>
 __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars bars,
                               volatile int* abort, uint32_t tmem) {
     using St = Storage<T>;
@@ -427,22 +428,31 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 }
                 if (edge) hide_columns(s, lim - j0 - 32 * q, low - j0 - 32 * q);
                 if (MOD) tmem_st32(tS + 32 * q, s);
+                if (MOD || EB == 2 || WIDE) {
+                    float m = max3(s[0], s[1], s[2]);
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    float m = max3(s[e], s[e + 1], s[e + 2]);
-                    m = max3(m, s[e + 3], s[e + 4]);
-                    m = max3(m, s[e + 5], s[e + 6]);
-                    m = fmaxf(m, s[e + 7]);
+                    for (int e = 3; e < 31; e += 2) m = max3(m, s[e], s[e + 1]);
+                    m = fmaxf(m, s[31]);
                     if (!MOD) {
                         float f = mul, lv = 0.f;
                         if (EB == 1) {
-                            const float4 kv = sc->kv[(32 * q + e) >> box];
+                            const float4 kv = sc->kv[(32 * q) >> box];
                             f = fmaxf(f * kv.x, 1e-37f);
                             lv = kv.z;
                         }
                         m = fmaf(m, f, lv);
                     }
                     top = fmaxf(top, m);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float m = max3(s[e], s[e + 1], s[e + 2]);
+                        m = max3(m, s[e + 3], s[e + 4]);
+                        m = max3(m, s[e + 5], s[e + 6]);
+                        m = fmaxf(m, s[e + 7]);
+                        const float4 kv = sc->kv[(32 * q + e) >> box];
+                        top = fmaxf(top, fmaf(m, fmaxf(mul * kv.x, 1e-37f), kv.z));
+                    }
                 }
             }
             // the last tile's decision, then this one's; a raised reference also
@@ -482,14 +492,14 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 tmem_ld32(tS + 32 * q, s);
                 if (!MOD && edge) hide_columns(s, lim - j0 - 32 * q, low - j0 - 32 * q);
                 uint32_t w[EB == 1 ? 24 : 16];
+                float f = MOD ? 1.f : mul, lv = off, ivs = 1.f;
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
-                    float f = MOD ? 1.f : mul, lv = off, ivs = 1.f;
-                    if (EB == 1) {
+                    if (EB == 1 && (e == 0 || !WIDE)) {
                         const float4 kv = sc->kv[(32 * q + e) >> box];
                         if (!MOD) {
-                            f = fmaxf(f * kv.x, 1e-37f);
-                            lv += kv.z;
+                            f = fmaxf(mul * kv.x, 1e-37f);
+                            lv = off + kv.z;
                         }
                         ivs = kv.w;
                         sum = make_float2(0.f, 0.f);
@@ -504,7 +514,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                         sum = add2(sum, make_float2(x[i], x[i + 1]));
                     }
                     if (EB == 1) {
-                        l = fmaf(sum.x + sum.y, ivs, l);
+                        if (e == 24 || !WIDE) l = fmaf(sum.x + sum.y, ivs, l);
 #pragma unroll
                         for (int i = 0; i < 8; i += 4) {
                             uint32_t part[3];
@@ -527,27 +537,10 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 if (!warp_wait(bars.v_full(stage), sph, abort)) return;
                 const int j = j0 + r;
                 unsigned char* vrow = sV0 + stage * nvb * kTS * 128 + r * 128;
-                const bool some = j <= it.last && j >= it.lo;
-                const bool all = j <= it.first && (a.window == 0 || j > it.last - a.window);
-                if (!some) {
-                    for (int b = 0; b < nvb; ++b)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4*>(vrow + b * kTS * 128 + i * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                } else if (!all) {
-                    for (int b = 0; b < nvb; ++b)
-#pragma unroll 4
-                        for (int i = 0; i < 32; ++i) {
-                            uint32_t* x = reinterpret_cast<uint32_t*>(vrow + b * kTS * 128) +
-                                          ((i + lane) & 31);
-                            const uint32_t v = *x, u = clear_odd<EB, T>(v, a.e5m2);
-                            if (u != v) {
-                                *x = u;
-                                *odd = k + 1;
-                            }
-                        }
-                }
+                const bool some_see = j <= it.last && j >= it.lo;
+                const bool all_see = j <= it.first && (a.window == 0 || j > it.last - a.window);
+                if (!all_see && clean_value_row<EB, T>(vrow, nvb, kTS * 128, some_see, a.e5m2))
+                    *odd = k + 1;
                 fence_async_shared();
             }
             tc_fence_before();
@@ -686,7 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     // the launch's 20 x 96
     if (warp < kSoft) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
-        softmax_warps<T, EB, MOD>(p, smem, bars, abort, tmem);
+        if (EB == 2 || p.hh >= 32)
+            softmax_warps<T, EB, MOD, true>(p, smem, bars, abort, tmem);
+        else
+            softmax_warps<T, EB, MOD, EB == 2>(p, smem, bars, abort, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kSWarp) {

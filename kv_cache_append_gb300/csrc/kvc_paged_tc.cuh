@@ -160,7 +160,9 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
         if (w < warp) before += v;
         total += v;
     }
-    const long long per = (total + p.ctas - 1) / p.ctas;
+    const long long per = total < (1ll << 31)
+                              ? (static_cast<uint32_t>(total) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)
+                              : (total + p.ctas - 1) / p.ctas;
     const long long at = static_cast<long long>(blockIdx.x) * per;
     long long cur = before + incl - mine;
     if (threadIdx.x == 0) {
@@ -241,7 +243,8 @@ struct PagedWalk {
             }
         }
         const int n = paged_group<TS>(p.a, p.RG, s.S, s.K, i).nt;
-        hk = static_cast<int>(off / n);
+        hk = off < (1ll << 31) ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(n))
+                               : static_cast<int>(off / n);
         tt = static_cast<int>(off - static_cast<long long>(hk) * n);
     }
     // The next run into `it`; false at the end.
@@ -277,15 +280,17 @@ struct PagedWalk {
 
 // The record of a block whose first run continues a unit: which unit, and the
 // blocks it lies in. Written for every block at every call.
-__device__ __forceinline__ void paged_record(const PagedTcParams& p, const PagedItem* it,
-                                             long long unit_start, int unit_tiles, long long per) {
+__device__ __forceinline__ void paged_record(const PagedTcParams& p, const PagedItem* it, int before,
+                                             int unit_tiles, long long per) {
     PagedRec r{};
     if (it) {
+        // `before` of the unit's tiles lie in earlier blocks; each block has a run of per
+        const uint32_t run = static_cast<uint32_t>(min(per, 1ll << 30));
         r.valid = 1;
         r.q0 = it->q0; r.r0 = it->r0; r.hk = it->hk;
         r.rows = min(p.RG, it->S * p.a.G - it->r0);
-        r.c0 = static_cast<int>(unit_start / per);
-        r.c1 = static_cast<int>((unit_start + unit_tiles - 1) / per);
+        r.c0 = static_cast<int>(blockIdx.x - (before + run - 1) / run);
+        r.c1 = static_cast<int>(blockIdx.x + (unit_tiles - before - 1) / run);
     }
     p.rec[blockIdx.x] = r;
 }
@@ -485,6 +490,48 @@ __device__ __forceinline__ uint32_t clear_odd(uint32_t w, bool e5m2) {
             if (((w >> (8 * i)) & 0x7fu) >= inf) keep &= ~(0xffu << (8 * i));
     }
     return w & keep;
+}
+
+// Nonzero when one of a word's elements is an infinity or NaN.
+template <int EB, typename T>
+__device__ __forceinline__ uint32_t has_odd(uint32_t w, bool e5m2) {
+    // the exponent (and for e4m3 the whole magnitude) all ones: one more carries out of it
+    const uint32_t field = EB == 2 ? (std::is_same<T, __nv_bfloat16>::value ? 0x7f807f80u : 0x7c007c00u)
+                                   : (e5m2 ? 0x7c7c7c7cu : 0x7f7f7f7fu);
+    const uint32_t one = EB == 2 ? (std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u)
+                                 : (e5m2 ? 0x04040404u : 0x01010101u);
+    return ((w & field) + one) & (EB == 2 ? 0x80008000u : 0x80808080u);
+}
+
+// A slot's value row in shared memory (eight 16-byte chunks in each of nvb column
+// blocks): cleared where no query row sees the slot, and of infinities and NaN where
+// some do and some do not; true where there were any of those.
+template <int EB, typename T>
+__device__ __forceinline__ bool clean_value_row(unsigned char* row, int nvb, int block_bytes, bool some,
+                                                bool e5m2) {
+    bool found = false;
+    for (int b = 0; b < nvb; ++b) {
+        uint4* v = reinterpret_cast<uint4*>(row + b * block_bytes);
+        if (!some) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 w = v[(i + threadIdx.x) & 7];
+            any |= has_odd<EB, T>(w.x, e5m2) | has_odd<EB, T>(w.y, e5m2) | has_odd<EB, T>(w.z, e5m2) |
+                   has_odd<EB, T>(w.w, e5m2);
+        }
+        if (any) {
+            found = true;
+            uint32_t* w = reinterpret_cast<uint32_t*>(v);
+#pragma unroll 1
+            for (int i = 0; i < 32; ++i) w[i] = clear_odd<EB, T>(w[i], e5m2);
+        }
+    }
+    return found;
 }
 
 }  // namespace kvc
