@@ -418,7 +418,7 @@ KVC_API int kvc_attend_paged(const kvc_paged_dims *dims, const int64_t *q_stride
 
 /*
  * The kernel kvc_attend_paged takes for these sizes with 16-byte aligned pools
- * and queries: "decode" or "rows" (tensor cores, for at most 32 query rows
+ * and queries: "decode" or "rows" (tensor cores, for at most 16 query rows
  * max_q * Hq / Hk of a KV head, or more; 16-bit queries, pool rows of whole
  * 16-byte words, D <= 256, Dv <= 128, block_size a multiple of 8), or "cores"
  * (CUDA cores: any size). Static text, or

@@ -239,7 +239,7 @@ struct PagedTcParams {
         return static_cast<int>((static_cast<uint64_t>(slot) * bs_mul) >> bs_shift);
     }
 };
-// Units of up to 32 query rows; nr: 4, 8, 16 or 32 (>= the rows of a unit).
+// Units of up to 16 query rows; nr: 4, 8 or 16 (>= the rows of a unit).
 cudaError_t launch_paged_decode(const PagedTcParams& p, int dtype, int pool_dtype, int nr,
                                 size_t smem, cudaStream_t stream);
 // Units in groups of 128 query rows.

@@ -95,6 +95,10 @@ struct TcPlan {
     int64_t bytes = 0, off_ml = 0, off_acc = 0;
     PagedTcParams p;
 };
+// Units of up to this many query rows take the decode kernel. 64 sequences of 1024 to
+// 8190 slots, 8 KV heads: at 16 rows decode 212 us and rows 252 on an 8-bit pool (230
+// and 247 on bf16), at 32 rows 312 and 252 (262 and 254).
+constexpr int64_t kDecodeRows = 16;
 constexpr int64_t kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024, kSmemReserved = 1024;
 
 // records of the blocks, then their partials
@@ -120,7 +124,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
     while ((int64_t(1) << l) < d.block_size) ++l;
     p.bs_shift = static_cast<uint32_t>(30 + l);
     p.bs_mul = static_cast<uint32_t>(((int64_t(1) << (30 + l)) + d.block_size - 1) / d.block_size);
-    if (R > 32) {
+    if (R > kDecodeRows) {
         // groups of 128 rows: query buffers, then rings of key and value tiles
         const int64_t parts = es == 1 ? 2 : 1, nkb = (d.D * es + 127) / 128, nvb = (d.Dv * es + 127) / 128;
         const int64_t kb = nkb * 128 * 128, vb = nvb * 128 * 128;
@@ -146,15 +150,15 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         tc_workspace(d, &t);
         return t;
     }
-    t.nr = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
-    const int64_t dn = t.nr <= 16 ? 16 : 32, parts = es == 1 ? 2 : 1;
+    t.nr = R <= 4 ? 4 : R <= 8 ? 8 : 16;
+    const int64_t dn = 16, parts = es == 1 ? 2 : 1;
     const int64_t nkb = (d.D * es + 127) / 128, nvb = es == 1 ? 1 : 2, nblk = dn * 128;
     p.RG = t.nr;
     p.hh = 128;
     while (d.block_size % p.hh != 0) p.hh /= 2;
     p.stage_bytes = static_cast<int>((nkb + nvb) * 128 * 128);
     p.q_bytes = static_cast<int>(parts * nkb * nblk);
-    const int64_t npt = es == 2 && dn == 16 ? 2 : 1;
+    const int64_t npt = es == 2 ? 2 : 1;
     p.ni = 2;
     auto layout = [&](int64_t stages, int64_t cap) {  // scales, items, exchange, queries, weights, stages
         p.off_item = static_cast<int>(512 + std::max<int64_t>(320, stages * 256));
@@ -164,9 +168,8 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         p.off_stage = static_cast<int>(p.off_p + npt * (es == 1 ? 3 : 2) * nblk);
         p.ns = static_cast<int>(std::min(stages, (cap - p.off_stage) / p.stage_bytes));
     };
-    // two blocks an SM where each still has two stages or more (not for 32 rows,
-    // whose registers take a whole SM)
-    int64_t blocks = es == 1 && t.nr <= 16 ? 2 : 1;
+    // two blocks an SM where each still has two stages or more
+    int64_t blocks = es == 1 ? 2 : 1;
     if (blocks == 2) {
         layout(3, kSmemSm / 2 - kSmemReserved);
         if (p.ns < 2) blocks = 1;

@@ -1,11 +1,11 @@
 // kvc_paged_decode.cu -- attention over a paged pool on the tensor cores, for
-// units (sequence, KV head) of at most 32 query rows: decode and short
+// units (sequence, KV head) of at most 16 query rows: decode and short
 // speculative steps.
 //
 // A step reads each visible cache row once and does 2 R (D + Dv) operations on
 // it: memory bounds it once the arithmetic is off the CUDA cores. As in the
 // decode kernel of the step, a tile's 128 slots are the M dimension of both
-// products, the unit's rows (padded to N = 16 or 32) the N dimension:
+// products, the unit's rows (padded to N = 16) the N dimension:
 //
 //   S^T  = K Q^T      (A = K tile as TMA wrote it, B = query rows)
 //   O^T += V^T P^T    (A = V tile read M-major, B = P^T from shared memory)
@@ -76,21 +76,22 @@ constexpr int kTmemSlot = 312, kAbort = 316, kBad = 320 /* [4] */, kOdd = 336 /*
 // What a run holds besides the query rows: per row the factor of its
 // products, its position (-1: no row) and its bias slope (times log2 e).
 struct RowData {
-    float mul[32];
+    float mul[32];  // (16 rows; a whole warp writes the rest)
     int lim[32];
     float slope[32];
 };
 
-template <int EB, int DN>
+constexpr int DN = 16;  // a unit's rows padded: N of the products
+template <int EB>
 struct Shape {
     static constexpr int kParts = EB == 1 ? 2 : 1;         // of a query row
     static constexpr int kWParts = EB == 1 ? 3 : 1;        // of a weight
     static constexpr int nblk = DN * 128;                  // a 128-byte column block of Q or P^T
     static constexpr int pblks = EB == 1 ? 1 : 2;          // column blocks of 128 weights
     static constexpr int pbytes = kWParts * pblks * nblk;  // one P^T buffer
-    static constexpr int npt = (EB == 2 && DN == 16) ? 2 : 1;  // P^T buffers
+    static constexpr int npt = EB == 2 ? 2 : 1;  // P^T buffers (one leaves 8-bit pools a third stage)
     static constexpr uint32_t col_o = 2 * DN;
-    static constexpr uint32_t cols = DN == 16 ? 64 : 128;
+    static constexpr uint32_t cols = 64;
 };
 
 template <int NR, bool MAX>
@@ -120,10 +121,10 @@ __device__ __forceinline__ float reduce_rows(const float (&v)[NR]) {
     return a[0];
 }
 
-template <typename T, int EB, int DN>
+template <typename T, int EB>
 __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bars,
                            const PagedStart* st, volatile int* abort) {
-    using S = Shape<EB, DN>;
+    using S = Shape<EB>;
     const PagedAttendParams& a = p.a;
     const int lane = threadIdx.x & 31;
     PagedItem* items = reinterpret_cast<PagedItem*>(smem + p.off_item);
@@ -225,10 +226,10 @@ __device__ void producer_warp(const PagedTcParams& p, unsigned char* smem, Bars 
 }
 
 // One warp: S^T of every tile.
-template <typename T, int EB, int DN>
+template <typename T, int EB>
 __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
                          uint32_t tmem) {
-    using S = Shape<EB, DN>;
+    using S = Shape<EB>;
     const PagedAttendParams& a = p.a;
     const uint32_t stage0 = smem_addr(smem + p.off_stage);
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
@@ -287,10 +288,10 @@ __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars,
 }
 
 // One warp: O^T += V^T P^T of every tile; releases the stages.
-template <typename T, int EB, int DN>
+template <typename T, int EB>
 __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars, volatile int* abort,
                           uint32_t tmem) {
-    using S = Shape<EB, DN>;
+    using S = Shape<EB>;
     const PagedAttendParams& a = p.a;
     const uint32_t stage0 = smem_addr(smem + p.off_stage);
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + p.off_item);
@@ -352,9 +353,8 @@ __device__ void pv_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars
 template <typename T, int EB, int NRT, int SG, bool MOD>
 __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars bars,
                               volatile int* abort, uint32_t tmem, const PagedStart* st) {
-    constexpr int DN = NRT <= 16 ? 16 : 32;
     constexpr int NR = NRT / SG;  // rows of this thread's group
-    using S = Shape<EB, DN>;
+    using S = Shape<EB>;
     using St = Storage<T>;
     const PagedAttendParams& a = p.a;
     const int t = threadIdx.x & 127;  // slot of the tile; value column of O^T
@@ -412,10 +412,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 return;
             tc_fence_after();
             float sv[NR];
-            if constexpr (NR == 32)
-                tmem_ld32(trow + sb * DN, sv);
-            else
-                tmem_ldn<NR>(trow + sb * DN, sv);
+            tmem_ldn<NR>(trow + sb * DN, sv);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.s_free(sb), 1u);
@@ -534,16 +531,10 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
                 if (!wait_pv(c - 1)) return;
                 tc_fence_after();
                 float ov[NR];
-                if constexpr (NR == 32)
-                    tmem_ld32(trow + S::col_o, ov);
-                else
-                    tmem_ldn<NR>(trow + S::col_o, ov);
+                tmem_ldn<NR>(trow + S::col_o, ov);
 #pragma unroll
                 for (int r = 0; r < NR; ++r) ov[r] *= corr[r];
-                if constexpr (NR == 32)
-                    tmem_st32(trow + S::col_o, ov);
-                else
-                    tmem_stn<NR>(trow + S::col_o, ov);
+                tmem_stn<NR>(trow + S::col_o, ov);
             }
             fence_async_shared();  // the weights and cleared value rows, for the tensor cores
             tc_fence_before();
@@ -555,10 +546,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         if (!wait_pv(c - 1)) return;
         tc_fence_after();
         float ov[NR];
-        if constexpr (NR == 32)
-            tmem_ld32(trow + S::col_o, ov);
-        else
-            tmem_ldn<NR>(trow + S::col_o, ov);
+        tmem_ldn<NR>(trow + S::col_o, ov);
         tc_fence_before();
         const uint32_t bm = rv & 1u;
         const float mine = reduce_rows<NR, false>(lsum);
@@ -616,10 +604,9 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
 }
 
 template <typename T, int EB, int NR, int SG, bool MOD>
-__global__ void __launch_bounds__(Roles<SG>::threads, EB == 1 && NR <= 16 ? 2 : 1)
+__global__ void __launch_bounds__(Roles<SG>::threads, EB == 1 ? 2 : 1)
     paged_decode_kernel(const __grid_constant__ PagedTcParams p) {
-    constexpr int DN = NR <= 16 ? 16 : 32;
-    using S = Shape<EB, DN>;
+    using S = Shape<EB>;
     using R = Roles<SG>;
     constexpr int kThreads = R::threads;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -667,13 +654,13 @@ __global__ void __launch_bounds__(Roles<SG>::threads, EB == 1 && NR <= 16 ? 2 : 
     if (warp < R::soft) {
         softmax_warps<T, EB, NR, SG, MOD>(p, smem, bars, abort, tmem, st);
     } else if (warp == R::s) {
-        s_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
+        s_issuer<T, EB>(p, smem, bars, abort, tmem);
     } else if (warp == R::pv) {
-        pv_issuer<T, EB, DN>(p, smem, bars, abort, tmem);
+        pv_issuer<T, EB>(p, smem, bars, abort, tmem);
     } else if (warp == R::prod) {
         producer_warp<EB>(p, smem, bars, abort);
     } else {
-        sched_warp<T, EB, DN>(p, smem, bars, st, abort);
+        sched_warp<T, EB>(p, smem, bars, st, abort);
     }
     tc_fence_before();
     __syncthreads();  // every thread reaches this exactly once: all waits are bounded
@@ -779,7 +766,7 @@ cudaError_t launch_t(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
 template <typename T, int EB, int NR>
 cudaError_t launch_nr(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
     // where a block has the SM to itself, two softmax groups from 8 rows on
-    constexpr int SG = EB == 1 ? (NR == 32 ? 2 : 1) : (NR >= 8 ? 2 : 1);
+    constexpr int SG = EB == 2 && NR >= 8 ? 2 : 1;
     return p.a.softcap > 0.f || p.a.slopes ? launch_t<T, EB, NR, SG, true>(p, smem, stream)
                                            : launch_t<T, EB, NR, SG, false>(p, smem, stream);
 }
@@ -788,8 +775,7 @@ cudaError_t launch_eb(const PagedTcParams& p, int nr, size_t smem, cudaStream_t 
     switch (nr) {
         case 4: return launch_nr<T, EB, 4>(p, smem, stream);
         case 8: return launch_nr<T, EB, 8>(p, smem, stream);
-        case 16: return launch_nr<T, EB, 16>(p, smem, stream);
-        default: return launch_nr<T, EB, 32>(p, smem, stream);
+        default: return launch_nr<T, EB, 16>(p, smem, stream);
     }
 }
 
@@ -807,7 +793,7 @@ cudaError_t launch_paged_decode(const PagedTcParams& p, int dtype, int pool_dtyp
 template <typename T>
 static cudaError_t launch_merge_t(const PagedTcParams& p, cudaStream_t stream) {
     // few rows: more warps for each (a long context's unit can have hundreds of partials)
-    const int wpr = p.RG <= 16 ? 4 : p.RG <= 32 ? 2 : 1, per = kMergeWarps / wpr;
+    const int wpr = p.RG <= 16 ? 4 : 1, per = kMergeWarps / wpr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>((p.RG + per - 1) / per));
     cfg.blockDim = dim3(kMergeWarps * 32);
@@ -817,9 +803,8 @@ static cudaError_t launch_merge_t(const PagedTcParams& p, cudaStream_t stream) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return wpr == 4   ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 4>, p)
-           : wpr == 2 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 2>, p)
-                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 1>, p);
+    return wpr == 4 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 4>, p)
+                    : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 1>, p);
 }
 
 cudaError_t launch_paged_merge(const PagedTcParams& p, int dtype, cudaStream_t stream) {

@@ -140,6 +140,12 @@ def _check(packed, key_pool, value_pool, key_scale, value_scale, block_table, cu
              _ints(seqlens_k, "seqlens_k", (B,), dev)), (T, Hq, D), (nb, Hk, bs, Dv))
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream's handle (torch.cuda.current_stream() without the
+    6 us that its Python object takes)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 class _OnDevice:
     """The inputs' device as the current one, where it is not already."""
 
@@ -243,7 +249,7 @@ def append_rotary_paged(query: torch.Tensor, new_key: torch.Tensor, new_value: t
             ctypes.byref(dims), 2 * c.shape[1], c.shape[0], int(bool(interleaved)), st, _ptr(q),
             _ptr(k), _ptr(v), _ptr(table), _ptr(cu), _ptr(kl), _ptr(c), _ptr(s), _ptr(key_pool),
             _ptr(value_pool), _ptr(key_scale), _ptr(value_scale), _ptr(out), status,
-            torch.cuda.current_stream(query.device).cuda_stream)
+            _raw_stream(query.device.index))
     if rc != 0:
         raise KvcError(rc, status_string(rc))
     return {"query": out, "key_pool": key_pool, "value_pool": value_pool, "key_scale": key_scale,
@@ -312,7 +318,7 @@ def attention_over_paged_cache(q: torch.Tensor, key_pool: torch.Tensor, value_po
             ctypes.byref(dims), st, _ptr(qq), _ptr(key_pool), _ptr(value_pool), _ptr(key_scale),
             _ptr(value_scale), _ptr(table), _ptr(cu), _ptr(kl), scale, softcap,
             _ptr(alibi_slopes), window, _ptr(out), _ptr(workspace), workspace.numel(), status,
-            torch.cuda.current_stream(q.device).cuda_stream)
+            _raw_stream(q.device.index))
     if rc != 0:
         raise KvcError(rc, status_string(rc))
     return out
