@@ -423,9 +423,9 @@ KVC_API int kvc_attend_paged(const kvc_paged_dims *dims, const int64_t *q_stride
  * 16-byte words, D <= 256, Dv <= 128, block_size a multiple of 8), or "cores"
  * (CUDA cores: any size). Static text, or
  * NULL for invalid dims. With an 8-bit pool the tensor-core kernels take a query
- * element as the sum of two e4m3 values (off by at most 2^-8 of it, or 2^-17 of
- * the row's largest) and a softmax weight as three e5m2 values (2^-9 of it, or
- * 2^-25 of the largest); with 16-bit pools a weight is rounded to the dtype.
+ * element as the sum of two or three e4m3 values (exact, but for 2^-17 of the row's
+ * largest) and a softmax weight as three e5m2 values (2^-9 of it, or 2^-25 of the
+ * largest); with 16-bit pools a weight is rounded to the dtype.
  */
 KVC_API const char *kvc_attend_paged_path(const kvc_paged_dims *dims);
 

@@ -101,6 +101,9 @@ struct TcPlan {
 constexpr int64_t kDecodeRows = 16;
 constexpr int64_t kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024, kSmemReserved = 1024;
 
+// 8-bit parts of a query element: bf16 2, fp16 3
+int64_t query_parts(const kvc_paged_dims& d) { return !eight(d) ? 1 : d.dtype == KVC_BF16 ? 2 : 3; }
+
 // records of the blocks, then their partials
 void tc_workspace(const kvc_paged_dims& d, TcPlan* t) {
     const PagedTcParams& p = t->p;
@@ -126,7 +129,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
     p.bs_mul = static_cast<uint32_t>(((int64_t(1) << (30 + l)) + d.block_size - 1) / d.block_size);
     if (R > kDecodeRows) {
         // groups of 128 rows: query buffers, then rings of key and value tiles
-        const int64_t parts = es == 1 ? 2 : 1, nkb = (d.D * es + 127) / 128, nvb = (d.Dv * es + 127) / 128;
+        const int64_t parts = query_parts(d), nkb = (d.D * es + 127) / 128, nvb = (d.Dv * es + 127) / 128;
         const int64_t kb = nkb * 128 * 128, vb = nvb * 128 * 128;
         p.RG = 128;
         p.hh = 128;
@@ -151,7 +154,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         return t;
     }
     t.nr = R <= 4 ? 4 : R <= 8 ? 8 : 16;
-    const int64_t dn = 16, parts = es == 1 ? 2 : 1;
+    const int64_t dn = 16, parts = query_parts(d);
     const int64_t nkb = (d.D * es + 127) / 128, nvb = es == 1 ? 1 : 2, nblk = dn * 128;
     p.RG = t.nr;
     p.hh = 128;
@@ -159,7 +162,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
     p.stage_bytes = static_cast<int>((nkb + nvb) * 128 * 128);
     p.q_bytes = static_cast<int>(parts * nkb * nblk);
     const int64_t npt = es == 2 ? 2 : 1;
-    p.ni = 2;
+    p.ni = parts == 3 && nkb == 1 ? 1 : 2;  // (one query buffer leaves fp16 a third stage)
     auto layout = [&](int64_t stages, int64_t cap) {  // scales, items, exchange, queries, weights, stages
         p.off_item = static_cast<int>(512 + std::max<int64_t>(320, stages * 256));
         p.off_x = p.off_item + 128 + 2 * 384;

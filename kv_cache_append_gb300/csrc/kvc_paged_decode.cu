@@ -11,10 +11,10 @@
 //   O^T += V^T P^T    (A = V tile read M-major, B = P^T from shared memory)
 //
 // 8-bit pools go to the tensor cores as they lie in memory (kind::f8f6f4), with
-// no conversion: the other operand is split into two 8-bit parts, and the
-// products of both parts add up in the same accumulator.
-//   Query rows: x 2^k = hi + lo, both e4m3, k from the row's largest element
-//   (2^7..2^8 then). 4 + 4 significant bits: bf16 exactly, fp16 to 2^-8 of an element.
+// no conversion: the other operand is split into 8-bit parts, and the
+// products of all parts add up in the same accumulator.
+//   Query rows: x 2^k as two e4m3 parts, three for fp16, k from the row's largest
+//   element (2^7..2^8 then): exact, but for what is under 2^-17 of that element.
 //   Weights: three e5m2 parts of an fp16 value (split_weights): 2^-9 of the weight
 //   over 16 octaves below the largest, 2^-25 of the largest under that. (e4m3 parts
 //   end at 2^-10: they would drop the flat rest behind one dominant slot of
@@ -84,7 +84,6 @@ struct RowData {
 constexpr int DN = 16;  // a unit's rows padded: N of the products
 template <int EB>
 struct Shape {
-    static constexpr int kParts = EB == 1 ? 2 : 1;         // of a query row
     static constexpr int kWParts = EB == 1 ? 3 : 1;        // of a weight
     static constexpr int nblk = DN * 128;                  // a 128-byte column block of Q or P^T
     static constexpr int pblks = EB == 1 ? 1 : 2;          // column blocks of 128 weights
@@ -262,7 +261,7 @@ __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars,
                     // the descriptor's address field
                     const uint64_t da = smem_desc_sw128(sK + b * kTS * 128, 16, 1024);
 #pragma unroll
-                    for (int part = 0; part < S::kParts; ++part) {
+                    for (int part = 0; part < QueryParts<T, EB>::v; ++part) {
                         const uint64_t db = smem_desc_sw128(sQ + (part * nkb + b) * S::nblk, 16, 1024);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {

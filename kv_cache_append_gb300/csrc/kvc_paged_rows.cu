@@ -7,11 +7,13 @@
 //   S  = Q K^T    (A = query rows, B = K tile, both from shared memory)
 //   O += P V      (A = P from tensor memory, B = V tile read N-major)
 //
-// With 8-bit pools both products take the tiles as they lie in memory, the
-// query rows as two e4m3 parts and the weights as three e5m2 parts (splits, scales
-// and references as in kvc_paged_decode.cu): five products at twice the 16-bit
-// rate against four halves, so the tensor-core time is 5/4 of 16-bit tiles', with
-// half the memory traffic and no conversion of the cache.
+// With 8-bit pools both products take the tiles as they lie in memory, the query
+// rows as two e4m3 parts (fp16: three) and the weights as three e5m2 parts (splits,
+// scales and references as in kvc_paged_decode.cu): five or six products at twice
+// the 16-bit rate against four halves, so the tensor-core time is 5/4 (3/2) of 16-bit
+// tiles', with half the memory traffic and no conversion of the cache. (Value tiles
+// turned into fp16 by four more warps, with weights of one part, took 1156 us where this
+// takes 1020: the conversion, 2300 cycles a tile, then was the longest stage.)
 //
 // The softmax, not the products, is the longer part of a tile, and a tile's chain
 // (S, softmax, P V, the next S into the same columns) is longer still: three groups
@@ -123,7 +125,7 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
             return;
         }
         unsigned char* sq = smem + p.off_q + kb * p.q_bytes;
-        float* mul = reinterpret_cast<float*>(sq + 2 * nkb * kBlk);  // 8-bit pools
+        float* mul = reinterpret_cast<float*>(sq + QueryParts<T, EB>::v * nkb * kBlk);  // 8-bit pools
         if (qw == 0 && lane == 0) {
             items[kb] = it;
             *reinterpret_cast<volatile int*>(smem + kBad + 4 * kb) = 0;
@@ -202,7 +204,7 @@ __device__ void s_issuer(const PagedTcParams& p, unsigned char* smem, Bars bars,
                          uint32_t tmem) {
     const PagedAttendParams& a = p.a;
     const PagedItem* items = reinterpret_cast<const PagedItem*>(smem + kItems);
-    constexpr int kParts = EB == 1 ? 2 : 1, kBlk = kRows * 128;
+    constexpr int kParts = QueryParts<T, EB>::v, kBlk = kRows * 128;
     const int nkb = (a.D * EB + 127) / 128, ksteps = (a.D * EB + 31) / 32;
     const uint32_t sK0 = smem_addr(smem + p.off_stage);
     const uint32_t idesc = EB == 1 ? mma_idesc_f8(kRows, kTS, false, a.e5m2, false, false)
@@ -371,7 +373,8 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         if (MOD && a.slopes && live) slope = a.slopes[it.hk * a.G + rr % a.G] * kLog2e;
         float mul = a.scale;
         if (EB == 1)
-            mul = reinterpret_cast<const float*>(smem + p.off_q + kb * p.q_bytes + 2 * nkb * kRows * 128)[r];
+            mul = reinterpret_cast<const float*>(smem + p.off_q + kb * p.q_bytes +
+                                                 QueryParts<T, EB>::v * nkb * kRows * 128)[r];
         if (!MOD) mul *= kLog2e;
         // the row's reference is one for all groups: tile n's warp reads what tile n -
         // 1's left, and may raise it

@@ -360,10 +360,19 @@ __device__ __forceinline__ void feed_copy(const PagedTcParams& p, const PagedIte
     __syncwarp();
 }
 
+// Parts of a query element for the 8-bit products, e4m3 each: 4 + 4 significant bits
+// hold a bfloat16, 4 + 4 + 4 an fp16 value (with two, fp16 scores were off by 2^-9
+// of their terms, ten times the rounding of an fp16 result).
+template <typename T, int EB>
+struct QueryParts {
+    static constexpr int v = EB == 2 ? 1 : std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
+};
+
 // A run's query rows into the swizzled operand layout, by THREADS threads, one or
-// two for a row (rows past the unit's are zero). 8-bit products: hi parts, then lo
-// parts, both e4m3, of the row times the power of two that takes its largest element
-// into [2^7, 2^8); mul[r] is the score scale over that power. (A warp for a row at a time
+// two for a row (rows past the unit's are zero). 8-bit products: the parts one after
+// the other, of the row times the power of two that takes its largest element into
+// [2^7, 2^8) (what is under 2^-17 of that is lost); mul[r] is the score scale over
+// that power. (A warp for a row at a time
 // needed a reduction and a division for each: 45 us for 128 rows of 192.)
 template <typename T, int EB, int ROWS, int THREADS>
 __device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const PagedItem& it,
@@ -418,7 +427,8 @@ __device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const Paged
     const float f = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
 #pragma unroll 1
     for (int c = part; c < nch; c += kPerRow) {
-        uint32_t hi[4], lo[4];
+        constexpr int NP = QueryParts<T, 1>::v;
+        uint32_t w[NP][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint2 v = word2(c * 16 + e * 4);
@@ -429,15 +439,23 @@ __device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const Paged
                 y[k] = Storage<T>::to_float(x[k]) * f;
                 if (!(fabsf(y[k]) < INFINITY)) y[k] = __uint_as_float(0x7fffffffu);  // no infinity: NaN
             }
-            const uint32_t h0 = to_eight2<false>(y[0], y[1]), h1 = to_eight2<false>(y[2], y[3]);
-            const float2 f0 = from_eight2<false>(h0), f1 = from_eight2<false>(h1);
-            hi[e] = h0 | (h1 << 16);
-            lo[e] = to_eight2<false>(y[0] - f0.x, y[1] - f0.y) |
-                    (to_eight2<false>(y[2] - f1.x, y[3] - f1.y) << 16);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const uint32_t h0 = to_eight2<false>(y[0], y[1]), h1 = to_eight2<false>(y[2], y[3]);
+                w[n][e] = h0 | (h1 << 16);
+                if (n + 1 < NP) {  // what is left, exactly
+                    const float2 f0 = from_eight2<false>(h0), f1 = from_eight2<false>(h1);
+                    y[0] -= f0.x;
+                    y[1] -= f0.y;
+                    y[2] -= f1.x;
+                    y[3] -= f1.y;
+                }
+            }
         }
         unsigned char* o = dst + (c >> 3) * blk + (((c & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(o + nkb * blk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            *reinterpret_cast<uint4*>(o + n * nkb * blk) = make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
     }
     if (part == 0) mul[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
 }

@@ -91,19 +91,20 @@ def dense(pool, scale, table, b, K):
     return x.permute(0, 2, 1, 3).reshape(-1, pool.shape[1], pool.shape[3])[:K]
 
 
-# Per kernel and pool kind: relative error of a query element and of a weight as
-# the products see them, beyond fp32 arithmetic.
+# Per kernel and pool kind: how far a query element (of the row's largest) and a
+# weight (of itself) are off as the products see them, beyond fp32 arithmetic.
 #   cores: fp32 throughout.
-#   tensor cores, 8-bit pools: a query element is the sum of two e4m3 values (each
-#   off by at most 2^-4 of what it rounds: 2^-8), a weight the sum of three e5m2
-#   values of its fp16 rounding, two cut to 3 bits and one rounded: 2^-9 + 2^-11, or 2^-25
-#   of the largest.
+#   tensor cores, 8-bit pools: the row is scaled so that its largest element lies
+#   in [2^7, 2^8), and an element is the sum of two e4m3 values (fp16: three), which hold
+#   its bits down to e4m3's last step, 2^-9: off by 2^-10, 2^-17 of the largest. A
+#   weight's fp16 rounding (2^-12) is the sum of three e5m2 values, two cut to 3 bits
+#   and one rounded: 2^-9 more, or 2^-25 of the largest weight.
 #   tensor cores, pools of the inputs' type: the query exact, a weight rounded to the type.
 def operand_errors(path, q_dtype, eight):
     if path == "cores":
         return 0.0, 0.0
     if eight:
-        return 2.0 ** -8, 2.0 ** -8
+        return 2.0 ** -17, 2.0 ** -9 + 2.0 ** -11
     return 0.0, UNIT[q_dtype]
 
 
@@ -136,7 +137,8 @@ def attend(q, key_pool, value_pool, table, cu, kl, key_scale=None, value_scale=N
             s = scale * (x @ kh.t())
             # a score's error: the query's rounding, fp32 products and sums (D + 8
             # roundings of terms), and 2^-20 of its size for the cap, bias and base change
-            err = scale * (x.abs() @ kh.abs().t()) * (eq + (D + 8) * u)
+            err = scale * ((x.abs() @ kh.abs().t()) * ((D + 8) * u)
+                           + eq * x.abs().amax(1, keepdim=True) * kh.abs().sum(1)[None])
             if softcap:
                 s = softcap * torch.tanh(s / softcap)
                 err = err + softcap * 2.0 ** -21
