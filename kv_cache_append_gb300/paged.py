@@ -52,9 +52,10 @@ def _paged_library() -> ctypes.CDLL:
 
 def make_paged_dims(B, total_q, max_q, Hq, Hk, D, Dv, num_blocks, block_size, max_blocks, dtype,
                     pool_dtype=None) -> PagedDims:
-    pool_dtype = dtype if pool_dtype is None else pool_dtype
-    code = _POOL_DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    pool = _POOL_DTYPES[pool_dtype] if isinstance(pool_dtype, torch.dtype) else int(pool_dtype)
+    """Sizes of one call; dtype and pool_dtype (default: the dtype) as torch
+    dtypes or kvc_dtype codes."""
+    code = _POOL_DTYPES.get(dtype, dtype)
+    pool = code if pool_dtype is None else _POOL_DTYPES.get(pool_dtype, pool_dtype)
     return PagedDims(B, total_q, max_q, Hq, Hk, D, Dv, num_blocks, block_size, max_blocks, code,
                      pool)
 
@@ -72,17 +73,17 @@ def attend_paged_workspace_bytes(dims: PagedDims) -> int:
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr() or None
+    return None if t is None else t.data_ptr()
 
 
 def _ints(t: torch.Tensor, name: str, shape, device) -> torch.Tensor:
+    if t.dtype == torch.int32 and t.shape == shape and t.device == device and t.is_contiguous():
+        return t
     if t.shape != shape or t.dtype.is_floating_point or t.dtype == torch.bool:
         raise ValueError(f"{name} must be integers of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if t.dtype != torch.int32:
-        t = t.to(torch.int32)
-    return t if t.is_contiguous() else t.contiguous()
+    return t.to(torch.int32).contiguous()
 
 
 def _check(packed, key_pool, value_pool, key_scale, value_scale, block_table, cu_seqlens_q,
@@ -146,20 +147,13 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-class _OnDevice:
-    """The inputs' device as the current one, where it is not already."""
-
-    def __init__(self, device):
-        index = device.index
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on_device(device, call, *args):
+    """call(*args, the device's current stream) with that device as the current one."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        return call(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return call(*args, _raw_stream(index))
 
 
 def _max_q(max_seqlen_q, cu, total_q) -> int:
@@ -243,13 +237,12 @@ def append_rotary_paged(query: torch.Tensor, new_key: torch.Tensor, new_value: t
     dims = make_paged_dims(table.shape[0], T, max_q, Hq, Hk, D, Dv, nb, bs, table.shape[1],
                            query.dtype, key_pool.dtype)
     st = (ctypes.c_int64 * 6)(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2])
-    status = _ptr(_status(status, query.device))
-    with _OnDevice(query.device):
-        rc = lib.kvc_append_rotary_paged(
-            ctypes.byref(dims), 2 * c.shape[1], c.shape[0], int(bool(interleaved)), st, _ptr(q),
-            _ptr(k), _ptr(v), _ptr(table), _ptr(cu), _ptr(kl), _ptr(c), _ptr(s), _ptr(key_pool),
-            _ptr(value_pool), _ptr(key_scale), _ptr(value_scale), _ptr(out), status,
-            _raw_stream(query.device.index))
+    rc = _on_device(
+        query.device, lib.kvc_append_rotary_paged, ctypes.byref(dims), 2 * c.shape[1], c.shape[0],
+        1 if interleaved else 0, st, q.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(),
+        cu.data_ptr(), kl.data_ptr(), c.data_ptr(), s.data_ptr(), key_pool.data_ptr(),
+        value_pool.data_ptr(), _ptr(key_scale), _ptr(value_scale), out.data_ptr(),
+        _ptr(_status(status, query.device)))
     if rc != 0:
         raise KvcError(rc, status_string(rc))
     return {"query": out, "key_pool": key_pool, "value_pool": value_pool, "key_scale": key_scale,
@@ -312,13 +305,11 @@ def attention_over_paged_cache(q: torch.Tensor, key_pool: torch.Tensor, value_po
             not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     st = (ctypes.c_int64 * 2)(*qq.stride()[:2])
-    status = _ptr(_status(status, q.device))
-    with _OnDevice(q.device):
-        rc = lib.kvc_attend_paged(
-            ctypes.byref(dims), st, _ptr(qq), _ptr(key_pool), _ptr(value_pool), _ptr(key_scale),
-            _ptr(value_scale), _ptr(table), _ptr(cu), _ptr(kl), scale, softcap,
-            _ptr(alibi_slopes), window, _ptr(out), _ptr(workspace), workspace.numel(), status,
-            _raw_stream(q.device.index))
+    rc = _on_device(
+        q.device, lib.kvc_attend_paged, ctypes.byref(dims), st, qq.data_ptr(), key_pool.data_ptr(),
+        value_pool.data_ptr(), _ptr(key_scale), _ptr(value_scale), table.data_ptr(), cu.data_ptr(),
+        kl.data_ptr(), scale, softcap, _ptr(alibi_slopes), window, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _ptr(_status(status, q.device)))
     if rc != 0:
         raise KvcError(rc, status_string(rc))
     return out
