@@ -364,7 +364,8 @@ typedef struct {
  * value's, divided by the scale and rounded once, ties to even, ending at the
  * format's largest; non-finite inputs take no part in the scale (infinities are
  * stored as the largest, NaN as NaN). A held scale that is no power of two is
- * kept while it suffices; values are then divided in fp32 first.
+ * kept while it suffices; values are then divided in fp32 first. An 8-bit block
+ * is at most 2^30 / max(D, Dv) slots (KVC_E_SHAPE).
  *
  * A sequence whose table has an id outside [0, num_blocks) among its new
  * slots' blocks is outside the contract too. The blocks that sequences write
@@ -391,7 +392,9 @@ KVC_API int kvc_append_rotary_paged(const kvc_paged_dims *dims, int64_t rotary_d
  *
  *   q_strides     host, 2 element strides: token and head (the last axis contiguous).
  *   q             [T, Hq, D] device, dtype.
- *   softcap       >= 0, finite; 0: no cap.
+ *   scale, softcap   scale > 0, softcap >= 0 (0: no cap), both finite. Below fp32's
+ *                 least normal value (2^-126), above 2^126, or with scale / softcap
+ *                 above that they are refused (KVC_E_SCALE).
  *   alibi_slopes  [Hq] device fp32, nullable.
  *   window        >= 0; 0: none. Blocks wholly before a window are not read.
  *   key_scale, value_scale   NULL unless the pool is in 8 bits; then positive,
@@ -425,7 +428,9 @@ KVC_API int kvc_attend_paged(const kvc_paged_dims *dims, const int64_t *q_stride
  * NULL for invalid dims. With an 8-bit pool the tensor-core kernels take a query
  * element as the sum of two or three e4m3 values (exact, but for 2^-17 of the row's
  * largest) and a softmax weight as three e5m2 values (2^-9 of it, or 2^-25 of the
- * largest); with 16-bit pools a weight is rounded to the dtype.
+ * largest); with 16-bit pools a weight is rounded to the dtype. An infinity in a
+ * query row over an 8-bit pool, or in an e5m2 key that the row sees, makes the row
+ * NaN, with a cap as well.
  */
 KVC_API const char *kvc_attend_paged_path(const kvc_paged_dims *dims);
 

@@ -3,6 +3,7 @@
 // synchronises.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -67,6 +68,9 @@ bool current_is_gb300() {
     return true;
 }
 
+// No sequence has more rows than there are.
+int64_t most_rows(const kvc_paged_dims& d) { return std::min(d.max_q, d.total_q); }
+
 // The CUDA-core kernel's splits of the slots: enough blocks for every SM to
 // hold a few, each with 256 slots or more of the capacity.
 struct CorePlan {
@@ -74,7 +78,7 @@ struct CorePlan {
 };
 CorePlan core_plan(const kvc_paged_dims& d) {
     const int64_t G = d.Hq / d.Hk, M = d.max_blocks * d.block_size;
-    const int64_t blocks = std::max<int64_t>(1, d.B * ((d.max_q * G + 7) / 8) * d.Hk);
+    const int64_t blocks = std::max<int64_t>(1, d.B * ((most_rows(d) * G + 7) / 8) * d.Hk);
     CorePlan c;
     c.nsplit = std::max<int64_t>(1, std::min({(4 * kPlanSms + blocks - 1) / blocks, M / 256,
                                               int64_t(64), 65535 / d.Hk}));
@@ -115,7 +119,7 @@ void tc_workspace(const kvc_paged_dims& d, TcPlan* t) {
 
 TcPlan tc_plan(const kvc_paged_dims& d) {
     TcPlan t;
-    const int64_t es = elem(d.pool_dtype), R = d.max_q * (d.Hq / d.Hk);
+    const int64_t es = elem(d.pool_dtype), R = most_rows(d) * (d.Hq / d.Hk);
     if (d.dtype == KVC_F32 || d.D * es % 16 != 0 || d.Dv * es % 16 != 0 || d.Dv > 128 ||
         d.block_size % 8 != 0 || d.total_q < 1)
         return t;
@@ -242,6 +246,8 @@ int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int6
     if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > d.D || num_positions < 0 ||
         num_positions > kMaxInt || (interleaved != 0 && interleaved != 1))
         return KVC_E_SHAPE;
+    // a block's 8-bit rows are counted in 31 bits
+    if (eight(d) && d.block_size > kMaxInt / std::max(d.D, d.Dv)) return KVC_E_SHAPE;
     const int64_t half = rotary_dim / 2;
     if (!strides || !block_table || !cu_seqlens_q || !seqlens_k || !key_pool || !value_pool ||
         (T > 0 && (!query || !new_key || !new_value || !out_query)) ||
@@ -279,7 +285,7 @@ int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int6
 
     AppendParams p;
     std::memset(&p, 0, sizeof(p));
-    p.B = d.B; p.total_q = T; p.max_q = d.max_q; p.M = d.max_blocks * d.block_size;
+    p.B = d.B; p.total_q = T; p.max_q = most_rows(d); p.M = d.max_blocks * d.block_size;
     p.max_blocks = d.max_blocks; p.num_blocks = static_cast<int>(d.num_blocks);
     p.Hq = static_cast<int>(d.Hq); p.Hk = static_cast<int>(d.Hk);
     p.D = static_cast<int>(d.D); p.Dv = static_cast<int>(d.Dv); p.bs = static_cast<int>(d.block_size);
@@ -314,7 +320,7 @@ int kvc_append_rotary_paged(const kvc_paged_dims* dims, int64_t rotary_dim, int6
     // 8-bit pools: small blocks, more of them on an SM (their two passes meet at barriers)
     p.threads = eight(d) && std::max(d.D - half, d.Dv) / ve <= 128 ? 128 : 256;
     if (eight(d)) {
-        p.seq_blocks = std::min<int64_t>((d.max_q + d.block_size - 2) / d.block_size + 1, d.max_blocks);
+        p.seq_blocks = std::min<int64_t>((p.max_q + d.block_size - 2) / d.block_size + 1, d.max_blocks);
         p.units8 = d.B * p.seq_blocks * d.Hk * 2;
     }
     return launch_append_rotary(p, d.dtype, d.pool_dtype == KVC_E4M3 ? 1 : d.pool_dtype == KVC_E5M2 ? 2 : 0,
@@ -353,7 +359,11 @@ int kvc_attend_paged(const kvc_paged_dims* dims, const int64_t* q_strides, const
         (eight(d) ? (!key_scale || !value_scale) : (key_scale || value_scale)))
         return KVC_E_NULL;
     if (!(scale > 0.0) || !std::isfinite(scale) || !(softcap >= 0.0) || !std::isfinite(softcap) ||
-        !std::isfinite(static_cast<float>(scale)) || !std::isfinite(static_cast<float>(softcap)))
+        softcap > FLT_MAX / 4)
+        return KVC_E_SCALE;
+    // what the kernels form of them stays a finite, normal fp32 value
+    if (scale < FLT_MIN || scale > FLT_MAX / 4 ||
+        (softcap > 0.0 && (softcap < FLT_MIN || scale / softcap > FLT_MAX / 4)))
         return KVC_E_SCALE;
     for (int i = 0; i < 2; ++i)
         if (q_strides[i] < 0 || q_strides[i] > (int64_t(1) << 40)) return KVC_E_SHAPE;
@@ -382,7 +392,7 @@ int kvc_attend_paged(const kvc_paged_dims* dims, const int64_t* q_strides, const
     const CorePlan c = core_plan(d);
     PagedAttendParams p;
     std::memset(&p, 0, sizeof(p));
-    p.B = d.B; p.total_q = T; p.max_q = d.max_q; p.M = d.max_blocks * d.block_size;
+    p.B = d.B; p.total_q = T; p.max_q = most_rows(d); p.M = d.max_blocks * d.block_size;
     p.max_blocks = d.max_blocks; p.num_blocks = static_cast<int>(d.num_blocks);
     p.Hq = static_cast<int>(d.Hq); p.Hk = static_cast<int>(d.Hk); p.G = static_cast<int>(d.Hq / d.Hk);
     p.D = static_cast<int>(d.D); p.Dv = static_cast<int>(d.Dv); p.bs = static_cast<int>(d.block_size);

@@ -208,8 +208,8 @@ __device__ __forceinline__ void token_rows(const AppendParams& p, const T* src, 
                     if (turn) x1[u] = *reinterpret_cast<const W*>(row + u * st_head + o1);
                 }
             float c[VE], sn[VE];
-            if (turn) {
-                const int64_t a = static_cast<int64_t>(max(at, 0)) * p.half + j * VE;
+            if (turn && at >= 0) {  // (a row outside the contract reads no angles: there may be none)
+                const int64_t a = static_cast<int64_t>(at) * p.half + j * VE;
                 load_angles<VE>(p.cos + a, c);
                 load_angles<VE>(p.sin + a, sn);
             }

@@ -19,6 +19,7 @@ from .kvc import DTYPES, KvcError, default_scale, library, status_string
 
 #: pool types in 8 bits, kept with one fp32 scale for each (block, head)
 EIGHT_BIT = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
+_INTEGERS = (torch.int8, torch.uint8, torch.int16, torch.int32, torch.int64)
 _POOL_DTYPES = {**DTYPES, **EIGHT_BIT}
 
 
@@ -79,10 +80,12 @@ def _ptr(t):
 def _ints(t: torch.Tensor, name: str, shape, device) -> torch.Tensor:
     if t.dtype == torch.int32 and t.shape == shape and t.device == device and t.is_contiguous():
         return t
-    if t.shape != shape or t.dtype.is_floating_point or t.dtype == torch.bool:
+    if t.shape != shape or t.dtype not in _INTEGERS:
         raise ValueError(f"{name} must be integers of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
+    if t.dtype == torch.int64:  # a value past 32 bits stays outside every range
+        t = t.clamp(-1, 2**31 - 1)
     return t.to(torch.int32).contiguous()
 
 

@@ -271,3 +271,33 @@ def test_side_stream_and_captured_graph(pool):
     graph.replay()
     torch.cuda.synchronize()
     check(y, {**g, "query": out}, False)
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_tables_without_positions(pool):
+    """cos / sin of no rows: every sequence is outside the contract; with no
+    turned elements the tables' length does not matter."""
+    x = on_gpu(make(23, "bf16", pool, [(3, 10), (1, 6)], 2, 1, 32, 32, 4, 32))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    keep = x["key_pool"].view(torch.uint8).clone()
+    z = {**x, "cos": x["cos"][:0], "sin": x["sin"][:0]}
+    got = kvc.append_rotary_paged(**z, status=status, max_seqlen_q=3)
+    assert int(status) == kvc.DEV_OVERFLOW and (got["query"] == 0).all()
+    assert torch.equal(x["key_pool"].view(torch.uint8), keep)
+    status.zero_()
+    z = {**x, "cos": x["cos"][:0, :0], "sin": x["sin"][:0, :0]}
+    got = kvc.append_rotary_paged(**z, status=status, max_seqlen_q=3)
+    assert int(status) == 0 and torch.equal(got["query"], x["query"])
+
+
+def test_wide_integers_are_not_wrapped():
+    x = on_gpu(make(24, "bf16", "bf16", [(2, 10), (1, 6)], 2, 1, 32, 32, 4, 32))
+    keep = x["key_pool"].clone()
+    y = {n: t.long() if n in ("block_table", "cu_seqlens_q", "seqlens_k") else t
+         for n, t in x.items()}
+    y["block_table"][0, 2] += 2 ** 32
+    y["seqlens_k"][1] += 2 ** 33
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = kvc.append_rotary_paged(**y, status=status, max_seqlen_q=2)
+    assert int(status) == kvc.DEV_OVERFLOW and (got["query"] == 0).all()
+    assert torch.equal(x["key_pool"], keep)

@@ -372,3 +372,89 @@ def test_append_then_attend(dtype, pool):
                  seqlens_k=kl, key_scale=ks, value_scale=vs)
         out = kvc.attention_over_paged_cache(**x, max_seqlen_q=max(new))
         check(x, out, max(new))
+
+
+@pytest.mark.parametrize("S", [1, 40])
+@pytest.mark.parametrize("dtype,pool", [("bf16", "e4m3"), ("f16", "f16")])
+def test_unaligned_pools_queries_and_outputs(dtype, pool, S):
+    """Tensors that start off a 16-byte boundary: the CUDA-core kernel, or (the
+    output of few rows) the same one, within the same bounds."""
+    x = make(31, dtype, pool, [(S, 300 + S), (S, S)], 4, 2, 64, 64, 16)
+
+    def shifted(t, by):
+        flat = torch.empty(t.numel() + by, dtype=torch.uint8 if t.element_size() == 1 else t.dtype,
+                           device="cuda")
+        flat[by:] = t.reshape(-1).view(flat.dtype)
+        return flat[by:].view(t.dtype).view(t.shape)
+
+    want, bound = ref.attend(x["q"], x["key_pool"], x["value_pool"], x["block_table"],
+                             x["cu_seqlens_q"], x["seqlens_k"], x["key_scale"], x["value_scale"],
+                             None, 0.0, None, 0, path_of(x, S))
+    for name in ("key_pool", "value_pool", "q", "out"):
+        y = dict(x)
+        out = None
+        if name == "out":
+            out = shifted(torch.zeros_like(x["q"]), 1)
+        else:
+            y[name] = shifted(x[name], 1)
+        got = kvc.attention_over_paged_cache(**y, max_seqlen_q=S, out=out)
+        assert ((got.double() - want).abs() <= bound).all(), name
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("S", [1, 24])
+def test_more_rows_announced_than_there_are(pool, S):
+    """max_seqlen_q may be any bound on the rows: past the packed rows it changes nothing."""
+    x = make(32, "bf16", pool, [(S, 500)], 4, 2, 64, 64, 16)
+    want = kvc.attention_over_paged_cache(**x, max_seqlen_q=S)
+    assert torch.equal(kvc.attention_over_paged_cache(**x, max_seqlen_q=10 ** 6), want)
+
+
+def test_wide_integers_are_not_wrapped():
+    x = make(33, "bf16", "bf16", [(1, 40), (1, 50)], 4, 2, 64, 64, 16)
+    want = kvc.attention_over_paged_cache(**x, max_seqlen_q=1)
+    y = {n: t.long() if n in ("block_table", "cu_seqlens_q", "seqlens_k") else t
+         for n, t in x.items()}
+    assert torch.equal(kvc.attention_over_paged_cache(**y, max_seqlen_q=1), want)
+    y["block_table"][0, 1] += 2 ** 32
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = kvc.attention_over_paged_cache(**y, max_seqlen_q=1, status=status)
+    assert int(status) == kvc.DEV_OVERFLOW
+    assert (got[0] == 0).all() and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError):
+        kvc.attention_over_paged_cache(**{**x, "seqlens_k": x["seqlens_k"].bool()}, max_seqlen_q=1)
+
+
+@pytest.mark.parametrize("pool", ["f16", "e5m2"])
+def test_two_calls_at_once(pool):
+    """Two streams, a workspace each, in turn over many rounds; and captured with
+    their own workspaces into one graph's two branches."""
+    x = make(34, "f16", pool, [(1, 3000), (1, 900), (1, 50)], 8, 2, 64, 64, 16)
+    z = make(35, "f16", pool, [(60, 700), (33, 33)], 8, 2, 64, 64, 16)
+    wx = kvc.attention_over_paged_cache(**x, max_seqlen_q=1)
+    wz = kvc.attention_over_paged_cache(**z, max_seqlen_q=60)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        with torch.cuda.stream(side[0]):
+            got[0].append(kvc.attention_over_paged_cache(**x, max_seqlen_q=1))
+        with torch.cuda.stream(side[1]):
+            got[1].append(kvc.attention_over_paged_cache(**z, max_seqlen_q=60))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, wx) for o in got[0]) and all(torch.equal(o, wz) for o in got[1])
+    ox, oz = torch.zeros_like(wx), torch.zeros_like(wz)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side[0].wait_stream(main)
+        with torch.cuda.stream(side[0]):
+            kvc.attention_over_paged_cache(**x, max_seqlen_q=1, out=ox)
+        kvc.attention_over_paged_cache(**z, max_seqlen_q=60, out=oz)
+        main.wait_stream(side[0])
+    for _ in range(3):
+        ox.zero_()
+        oz.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ox, wx) and torch.equal(oz, wz)

@@ -137,3 +137,20 @@ def test_workspace_holds_for_every_size(lib):
         assert n >= 256 and n % 256 == 0
         last = max(last, n)
     assert kvc.attend_paged_path(dims())
+
+
+def test_scales_outside_fp32_and_blocks_past_31_bits(lib):
+    d = dims()
+    for bad in (1e-39, 1e-300, 3e38):
+        assert attend(lib, d, scale=bad) == -4
+        assert attend(lib, d, softcap=bad) == -4
+    assert attend(lib, d, scale=1e10, softcap=1e-30) == -4
+    e = dims(pool_dtype=3, block_size=1 << 25, max_blocks=1)
+    assert append(lib, e) == -2
+
+
+def test_rows_past_the_packed_ones_do_not_change_the_plan():
+    for q in (4, 16):
+        a, b = dims(B=1, total_q=q, max_q=q), dims(B=1, total_q=q, max_q=10 ** 6)
+        assert kvc.attend_paged_path(a) == kvc.attend_paged_path(b)
+        assert kvc.attend_paged_workspace_bytes(a) == kvc.attend_paged_workspace_bytes(b)
