@@ -38,6 +38,11 @@
 // could carry an infinity or NaN into the rows that do not: its thread then
 // clears those elements in the tile and the unit's epilogue adds them, from
 // memory, to the rows that see them.
+//
+// Measured: 64 tokens over 1024 to 8190 slots, 32 heads on 8 of 128, e4m3 pool (602 MB):
+// 113.5 us, 5300 GB/s, bounded by DRAM and 10 to 15 us of start and tail (4.2 GB of
+// cache: 6580 GB/s); 64 sequences of 1 to 4 tokens, cap, window 4096, bf16 pool (935 MB):
+// 196 us, 4770 GB/s, bounded by a tile's softmax chain with three stages an SM.
 #include <algorithm>
 #include <type_traits>
 
@@ -764,7 +769,8 @@ cudaError_t launch_t(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
 }
 template <typename T, int EB, int NR>
 cudaError_t launch_nr(const PagedTcParams& p, size_t smem, cudaStream_t stream) {
-    // where a block has the SM to itself, two softmax groups from 8 rows on
+    // where a block has the SM to itself, two softmax groups from 8 rows on (an 8-bit
+    // pool's two blocks an SM cover each other's softmax, 4 rows are too few to divide)
     constexpr int SG = EB == 2 && NR >= 8 ? 2 : 1;
     return p.a.softcap > 0.f || p.a.slopes ? launch_t<T, EB, NR, SG, true>(p, smem, stream)
                                            : launch_t<T, EB, NR, SG, false>(p, smem, stream);

@@ -12,8 +12,9 @@
 // scales and references as in kvc_paged_decode.cu): five or six products at twice
 // the 16-bit rate against four halves, so the tensor-core time is 5/4 (3/2) of 16-bit
 // tiles', with half the memory traffic and no conversion of the cache. (Value tiles
-// turned into fp16 by four more warps, with weights of one part, took 1156 us where this
-// takes 1020: the conversion, 2300 cycles a tile, then was the longest stage.)
+// turned into fp16 by four more warps, with weights of one part, took 1156 us where the
+// parts took 1020, in this kernel's state of that time: the conversion, 2300 cycles a
+// tile, then was the longest stage.)
 //
 // The softmax, not the products, is the longer part of a tile, and a tile's chain
 // (S, softmax, P V, the next S into the same columns) is longer still: three groups
@@ -29,6 +30,11 @@
 // softmax, an S issuer, a P.V issuer, a producer of key tiles and one of value tiles,
 // and 4 that schedule the block's runs (kvc_paged_tc.cuh) and prepare the next
 // run's query rows.
+//
+// Measured, 32 heads on 8 of 128, four prompts of 513 to 2001 tokens over up to 8190
+// slots (617 GFLOP): e4m3 pool 910 us, 680 TFLOP/s, bf16 pool 773 us; bounded by the
+// softmax warps' instruction fetch and issue (a tile takes about 3000 and 2000 cycles
+// where its products take 1280 and 1024).
 #include <algorithm>
 #include <type_traits>
 

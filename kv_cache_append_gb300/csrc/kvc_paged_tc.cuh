@@ -199,7 +199,7 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
 // The scheduling warp's walk over its block's runs (all lanes alike).
 template <int TS>
 struct PagedWalk {
-    long long left = 0, at = 0;  // tiles to hand out, the list index of the next
+    long long left = 0;  // tiles to hand out
     long long per = 1;
     int b = 0, i = 0, hk = 0, tt = 0;  // next tile: sequence, group, head, tile of the unit
     PagedSeq s{};
@@ -211,8 +211,7 @@ struct PagedWalk {
     }
     __device__ void start(const PagedTcParams& p, const PagedStart* st) {
         per = st->per;
-        at = static_cast<long long>(blockIdx.x) * per;
-        left = min(per, st->total - at);
+        left = min(per, st->total - static_cast<long long>(blockIdx.x) * per);
         if (left <= 0) return;
         b = st->b;
         load(p);
@@ -265,7 +264,6 @@ struct PagedWalk {
         it.flags = (tt == 0 ? kItemBegins : 0) | (tt + take == g.nt ? kItemEnds : 0);
         unit_tiles = g.nt;
         left -= take;
-        at += take;
         tt += take;
         if (tt == g.nt) {
             tt = 0;

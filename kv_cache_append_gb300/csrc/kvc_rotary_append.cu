@@ -23,6 +23,12 @@
 // A rotated value is formed exactly (two products as head and tail, their sum
 // rounded to odd in fp32), so the one rounding to 8 bits is that of the exact
 // value, whatever order or fusion the products are taken in.
+//
+// Measured (device time): one token 4.2 us and 64 tokens 4.9 us (7.9 us into an e4m3
+// pool), the launch and two dependent look-ups; 9600 f16 prompt tokens, 32 query heads on 8
+// of 128: 54.5 us, 4590 GB/s, bounded by each block's look-up before its one round of loads;
+// 16600 tokens, 16 query heads on one of 192 into an e4m3 pool: 73.5 us, 3980 GB/s,
+// bounded by the issue of the exact products and the barrier between the passes.
 #include <algorithm>
 
 #include "kvc_launch.h"
@@ -164,8 +170,9 @@ __device__ __forceinline__ bool append_bad_ids(const AppendParams& p, int64_t b,
 
 // Rows of `heads` heads for each of the block's tokens: a thread takes one job of
 // the rows of p.hg heads (kHeads, or one where tokens are few), whose loads are
-// all under way together and share the angles (one row at a time, the loads' latency held a prompt to 38% of the
-// copy bandwidth), and steps over such groups, so that nothing is divided in the loop.
+// all under way together and share the angles (one row at a time a prompt ran at 38% of
+// the copy bandwidth, now at 69%), and steps over such groups, so that nothing is
+// divided in the loop.
 constexpr int kHeads = 4;
 template <typename T, int VE, typename Dst>
 __device__ __forceinline__ void token_rows(const AppendParams& p, const T* src, int64_t tok0, int nt,
