@@ -225,6 +225,7 @@ struct PagedTcParams {
     PagedAttendParams a;
     int RG;            // query rows of a unit
     int ctas;          // blocks of the grid
+    int lead;          // places of the tile list that the start of a unit takes
     uint32_t bs_mul, bs_shift;  // slot / block_size = slot * bs_mul >> bs_shift (slots below 2^30)
     int hh;            // slots of a box: the largest power of two up to 128 dividing block_size
     int ns, ni;        // stages (rows kernel: of keys), item and query buffers

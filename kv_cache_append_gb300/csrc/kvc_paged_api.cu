@@ -103,6 +103,15 @@ struct TcPlan {
 // 8190 slots, 8 KV heads: at 16 rows decode 212 us and rows 252 on an 8-bit pool (230
 // and 247 on bf16), at 32 rows 312 and 252 (262 and 254).
 constexpr int64_t kDecodeRows = 16;
+// What the start of a unit takes of a block's time, in tiles: its first tile's latency,
+// its query rows, its result and the tiles at its mask's edge. Not counted, the blocks
+// with the most unit starts are the last to end. Rows kernel, at 0, 3, 6, 8 and 12
+// tiles: 32 prompts of 20 to 300 tokens over up to 4000 slots, 32 heads on 8, e4m3 646,
+// 411, 339, 339 and 356 us (bf16 685, 433, 346, 307, 295); 4 of 513 to 2001 over up to
+// 8190, 902, 822, 783, 772 and 767. Decode kernel, at 0, 1, 2 and 3: 64 tokens over 1024
+// to 8190 slots, e4m3 113.5, 110.3, 108.4 and 109.7 us; 200 over 100 to 2000 at 1, 2 and 3
+// 128.8, 121.0 and 117.5; 64 sequences of 1 to 4 tokens, cap, bf16 198, 185, 176 and 172.
+constexpr int kLeadRows = 8, kLeadDecode = 3;
 constexpr int64_t kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024, kSmemReserved = 1024;
 
 // 8-bit parts of a query element: bf16 2, fp16 3
@@ -129,6 +138,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
     // excess m d - 2^(30 + l) < d <= 2^l takes slot m / 2^(30 + l) less than 1 / d up
     int l = 0;
     while ((int64_t(1) << l) < d.block_size) ++l;
+    p.lead = R > kDecodeRows ? kLeadRows : kLeadDecode;
     p.bs_shift = static_cast<uint32_t>(30 + l);
     p.bs_mul = static_cast<uint32_t>(((int64_t(1) << (30 + l)) + d.block_size - 1) / d.block_size);
     if (R > kDecodeRows) {

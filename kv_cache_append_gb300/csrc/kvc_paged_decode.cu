@@ -135,7 +135,7 @@ __device__ void sched_warp(const PagedTcParams& p, unsigned char* smem, Bars bar
     const int nkb = (a.D * EB + 127) / 128;
     PagedWalk<kTS> w;
     w.start(p, st);
-    const int before = w.tt;
+    const int before = w.tt - w.lead;  // of the unit's tiles, in earlier blocks
     PagedItem it;
     int unit_tiles = 0;
     bool more = w.next(p, it, unit_tiles);

@@ -110,7 +110,7 @@ __device__ void query_warps(const PagedTcParams& p, unsigned char* smem, Bars ba
     constexpr int kBlk = kRows * 128;
     PagedWalk<kTS> w;  // each warp walks alike
     w.start(p, st);
-    const int before = w.tt;
+    const int before = w.tt - w.lead;  // of the unit's tiles, in earlier blocks
     PagedItem it;
     int unit_tiles = 0;
     bool more = w.next(p, it, unit_tiles);

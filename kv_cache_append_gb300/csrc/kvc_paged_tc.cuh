@@ -6,9 +6,12 @@
 // t G + g of a KV head are grouped in order. Its tiles are the runs of TS slots
 // (aligned to TS) from its first visible slot to its last. All units' tiles in
 // order (sequence, group, head) are one list; block c of the grid takes tiles [c per,
-// (c + 1) per). Every block computes the list's length itself from cu_seqlens
-// and seqlens_k (one pass over B sequences), so a call is one launch, whatever the
-// lengths, and no block has more than one tile more than another. A unit that lies
+// (c + 1) per). The start of a unit (its query rows, its first tile's latency, its
+// result) counts as p.lead further tiles before the first, which no block works on
+// (in a list that has a block for every tile, as none).
+// Every block computes the list's length itself from cu_seqlens and seqlens_k (one
+// pass over B sequences), so a call is one launch, whatever the lengths, and all blocks
+// have about the same to do. A unit that lies
 // within one block is finished there; of a unit cut between blocks each block
 // leaves a partial (at most two per block: the tail of a unit in slot 0, the
 // head of one in slot 1), which paged_merge_kernel joins.
@@ -86,8 +89,9 @@ struct PagedGroup {
     int tile0, nt;
 };
 template <int TS>
-__device__ __forceinline__ PagedGroup paged_group(const PagedAttendParams& a, int RG, int S, int K,
-                                                  int i) {
+__device__ __forceinline__ PagedGroup paged_group(const PagedTcParams& p, int S, int K, int i) {
+    const PagedAttendParams& a = p.a;
+    const int RG = p.RG;
     PagedGroup g;
     const int R = S * a.G, r0 = i * RG;
     g.first = K - S + r0 / a.G;
@@ -114,22 +118,29 @@ constexpr int kItemEnds = 2;    // the run ends the unit
 constexpr int kItemDone = 4;    // no more runs
 
 // Where a block's run of the tile list starts, found by all threads of it.
+constexpr int kPlanWarps = 20;  // of a block, at most
 struct PagedStart {
     long long total, per;
-    int b;          // sequence of the first tile
-    long long off;  // its tile within the sequence
-    long long sums[32];
+    int lead;       // places of the list that a unit's start takes
+    int b;          // sequence of the block's first place
+    long long off;  // its place within the sequence
+    long long sums[kPlanWarps];
+    int units[kPlanWarps];
 };
+static_assert(sizeof(PagedStart) <= 320, "the kernels keep 320 bytes for it");
 
 template <int TS>
-__device__ __forceinline__ long long paged_seq_tiles(const PagedTcParams& p, int64_t b, int* invalid) {
+__device__ __forceinline__ long long paged_seq_tiles(const PagedTcParams& p, int64_t b, int* invalid,
+                                                      int* units) {
     const PagedAttendParams& a = p.a;
     const PagedSeq s = paged_seq(a.cu, a.kl, b, a.total_q, a.max_q, a.M);
     if (!s.ok) *invalid = 1;
+    *units = 0;
     if (!s.ok || s.S == 0) return 0;
     long long n = 0;
     const int ng = paged_groups(a, p.RG, s.S);
-    for (int i = 0; i < ng; ++i) n += paged_group<TS>(a, p.RG, s.S, s.K, i).nt;
+    for (int i = 0; i < ng; ++i) n += paged_group<TS>(p, s.S, s.K, i).nt;
+    *units = ng * a.Hk;
     return n * a.Hk;
 }
 
@@ -143,38 +154,66 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
     const int64_t b0 = min(B, threadIdx.x * per_thread), b1 = min(B, b0 + per_thread);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long mine = 0;
-    int invalid = 0;
-    for (int64_t b = b0; b < b1; ++b) mine += paged_seq_tiles<TS>(p, b, &invalid);
+    int invalid = 0, mine_u = 0;
+    for (int64_t b = b0; b < b1; ++b) {
+        int u;
+        mine += paged_seq_tiles<TS>(p, b, &invalid, &u);
+        mine_u += u;
+    }
     long long incl = mine;
+    int incl_u = mine_u;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int u = __shfl_up_sync(0xffffffffu, incl_u, o);
+        if (lane >= o) {
+            incl += v;
+            incl_u += u;
+        }
     }
-    if (lane == 31) st->sums[warp] = incl;
+    static_assert(THREADS / 32 <= kPlanWarps, "a sum for every warp");
+    if (lane == 31) {
+        st->sums[warp] = incl;
+        st->units[warp] = incl_u;
+    }
     invalid = __syncthreads_or(invalid);
     long long before = 0, total = 0;
+    int before_u = 0, total_u = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         const long long v = st->sums[w];
-        if (w < warp) before += v;
+        const int u = st->units[w];
+        if (w < warp) {
+            before += v;
+            before_u += u;
+        }
         total += v;
+        total_u += u;
     }
+    // a block for every tile: nothing to level, and each takes one
+    const int lead = total <= p.ctas ? 0 : p.lead;
+    total += static_cast<long long>(lead) * total_u;
+    before += static_cast<long long>(lead) * (before_u + incl_u - mine_u);
+    const long long tiles = mine;
+    mine += static_cast<long long>(lead) * mine_u;
     const long long per = total < (1ll << 31)
                               ? (static_cast<uint32_t>(total) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)
                               : (total + p.ctas - 1) / p.ctas;
     const long long at = static_cast<long long>(blockIdx.x) * per;
-    long long cur = before + incl - mine;
+    long long cur = before + incl - tiles;
     if (threadIdx.x == 0) {
         st->total = total;
         st->per = per;
+        st->lead = lead;
     }
     if (per_thread == 1 && at >= cur && at < cur + mine) {
         st->b = static_cast<int>(b0);
         st->off = at - cur;
     } else if (at >= cur && at < cur + mine) {
         for (int64_t b = b0; b < b1; ++b) {
-            const long long n = paged_seq_tiles<TS>(p, b, &invalid);
+            int u;
+            long long n = paged_seq_tiles<TS>(p, b, &invalid, &u);
+            n += static_cast<long long>(lead) * u;
             if (at < cur + n) {
                 st->b = static_cast<int>(b);
                 st->off = at - cur;
@@ -199,8 +238,9 @@ __device__ __forceinline__ void paged_plan(const PagedTcParams& p, PagedStart* s
 // The scheduling warp's walk over its block's runs (all lanes alike).
 template <int TS>
 struct PagedWalk {
-    long long left = 0;  // tiles to hand out
+    long long left = 0;  // places to hand out
     long long per = 1;
+    int lead = 0;
     int b = 0, i = 0, hk = 0, tt = 0;  // next tile: sequence, group, head, tile of the unit
     PagedSeq s{};
     int ng = 0;
@@ -211,6 +251,7 @@ struct PagedWalk {
     }
     __device__ void start(const PagedTcParams& p, const PagedStart* st) {
         per = st->per;
+        lead = st->lead;
         left = min(per, st->total - static_cast<long long>(blockIdx.x) * per);
         if (left <= 0) return;
         b = st->b;
@@ -221,7 +262,7 @@ struct PagedWalk {
         for (i = 0;; i += 32) {
             long long n = 0;
             if (i + lane < ng)
-                n = static_cast<long long>(paged_group<TS>(p.a, p.RG, s.S, s.K, i + lane).nt) * p.a.Hk;
+                n = static_cast<long long>(paged_group<TS>(p, s.S, s.K, i + lane).nt + lead) * p.a.Hk;
             long long incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -241,7 +282,7 @@ struct PagedWalk {
                 return;
             }
         }
-        const int n = paged_group<TS>(p.a, p.RG, s.S, s.K, i).nt;
+        const int n = paged_group<TS>(p, s.S, s.K, i).nt + lead;
         hk = off < (1ll << 31) ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(n))
                                : static_cast<int>(off / n);
         tt = static_cast<int>(off - static_cast<long long>(hk) * n);
@@ -255,17 +296,20 @@ struct PagedWalk {
             i = 0;
             load(p);
         }
-        const PagedGroup g = paged_group<TS>(p.a, p.RG, s.S, s.K, i);
-        const int take = static_cast<int>(min(static_cast<long long>(g.nt - tt), left));
+        const PagedGroup g = paged_group<TS>(p, s.S, s.K, i);
+        const int take = static_cast<int>(min(static_cast<long long>(g.nt + lead - tt), left));
+        left -= take;
+        // its tiles among these places (none: they are the block's last)
+        const int t0 = max(tt - lead, 0), t1 = tt + take - lead;
+        if (t1 <= 0) return false;
         it.b = b; it.q0 = s.q0; it.S = s.S; it.K = s.K;
         it.r0 = i * p.RG; it.hk = hk;
         it.first = g.first; it.last = g.last; it.lo = g.lo;
-        it.tile0 = g.tile0 + tt; it.nt = take;
-        it.flags = (tt == 0 ? kItemBegins : 0) | (tt + take == g.nt ? kItemEnds : 0);
+        it.tile0 = g.tile0 + t0; it.nt = t1 - t0;
+        it.flags = (t0 == 0 ? kItemBegins : 0) | (t1 == g.nt ? kItemEnds : 0);
         unit_tiles = g.nt;
-        left -= take;
         tt += take;
-        if (tt == g.nt) {
+        if (tt == g.nt + lead) {
             tt = 0;
             if (++hk == p.a.Hk) {
                 hk = 0;
