@@ -148,7 +148,7 @@ TcPlan tc_plan(const kvc_paged_dims& d) {
         p.RG = 128;
         p.hh = 128;
         while (d.block_size % p.hh != 0) p.hh /= 2;
-        p.off_q = es == 1 ? 12288 : 8192;  // scales of 16 tiles, or none
+        p.off_q = es == 1 ? 16384 : 12288;  // behind the scales of 16 tiles, or none
         p.q_bytes = static_cast<int>(parts * kb + (es == 1 ? 1024 : 0));
         // the next run's query rows are prepared ahead where that leaves three tiles
         int64_t room = kSmemBlock - p.off_q - 2 * p.q_bytes;

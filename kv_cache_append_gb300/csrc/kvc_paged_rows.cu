@@ -64,18 +64,18 @@ struct Bars {
     // per 32 rows and group: one barrier for all would let a group that is two tiles
     // ahead of the decisions take an old phase for the one it waits for
     __device__ uint32_t decide(int w, int g) const { return base + 360u + 8u * (3 * w + g); }
-    __device__ uint32_t meet() const { return base + 456u; }
+    __device__ uint32_t meet(int k) const { return base + ((k & 1) ? 528u : 456u); }
     __device__ uint32_t o_free() const { return base + 464u; }
     __device__ uint32_t drained() const { return base + 472u; }
     // the run is known (its query rows are not ready yet)
     __device__ uint32_t item_known(int k) const { return base + 480u + 8u * k; }
 };
-constexpr int kTmemSlot = 496, kAbort = 500, kBad = 504 /* [2] */, kOdd = 512 /* [2] */;
+constexpr int kTmemSlot = 496, kAbort = 500, kBad = 504 /* [2] */, kOdd = 512 /* [3] */;
 constexpr int kStart = 576, kItems = 896;
-// exchanged between the groups, for even and odd runs: a row's reference [2][128],
-// each group's sum and the reference it is measured by [2][3][128]
-constexpr int kXr = 1024, kXl = 2048;
-constexpr int kScales = 8192, kScaleRing = 16;  // 8-bit pools: 16 tiles' scales
+// exchanged between the groups, for three runs in turn: a row's reference [3][128],
+// each group's sum and the reference it is measured by [3][3][128]
+constexpr int kXr = 1024, kXl = 2560;
+constexpr int kScales = 11776, kScaleRing = 16;  // 8-bit pools: 16 tiles' scales
 
 // Tile c's group (c % 3) and the parity of its use of that group's barriers.
 struct Turn {
@@ -370,7 +370,11 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         if (!warp_wait(bars.item_full(kb), static_cast<uint32_t>((k / p.ni) & 1), abort)) return;
         const PagedItem it = items[kb];
         if (it.flags & kItemDone) return;
-        volatile int* odd = reinterpret_cast<volatile int*>(smem + kOdd + 4 * (k & 1));
+        // a group that is done with its tiles goes on to the next run, at most two ahead
+        // of the last group: run k - 3's exchange buffers are free once all met in run k - 2
+        if (k >= 2 && !warp_wait(bars.meet(k), static_cast<uint32_t>((k >> 1) - 1) & 1u, abort)) return;
+        const int k3 = k % 3;
+        volatile int* odd = reinterpret_cast<volatile int*>(smem + kOdd + 4 * k3);
         const int rr = it.r0 + r;
         const bool live = rr < it.S * a.G;
         const int lim = live ? it.K - it.S + rr / a.G : -1;
@@ -384,8 +388,8 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         if (!MOD) mul *= kLog2e;
         // the row's reference is one for all groups: tile n's warp reads what tile n -
         // 1's left, and may raise it
-        float* xr = reinterpret_cast<float*>(smem + kXr) + (k & 1) * 128 + r;
-        float2* xl = reinterpret_cast<float2*>(smem + kXl) + (k & 1) * 3 * 128 + r;
+        float* xr = reinterpret_cast<float*>(smem + kXr) + k3 * 128 + r;
+        float2* xl = reinterpret_cast<float2*>(smem + kXl) + k3 * 3 * 128 + r;
         float ref = -INFINITY, l = 0.f;  // the reference that this group's sum is measured by
         for (int n = 0; n < it.nt; ++n, ++c) {
             const int stage = vr.s, tg = turn.g;
@@ -468,7 +472,8 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             // rescales O, at rest between the two tiles' products
             const int pg = g == 0 ? kGroups - 1 : g - 1;  // tile c - 1's group and parity
             const uint32_t pph = g == 0 ? tph ^ 1u : tph;
-            if (n > 0 && !warp_wait(bars.decide(wq, pg), pph, abort)) return;
+            // (a run's first tile waits too: no group's decisions are two ahead of another's)
+            if (c > 0 && !warp_wait(bars.decide(wq, pg), pph, abort)) return;
             const float was = n > 0 ? *xr : -INFINITY;
             const bool raise = top > was + RaiseAbove<EB>::v;
             const float now = raise ? top : was;
@@ -556,15 +561,19 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.p_ready(g), 1u);
         }
-        // the run's end: its last product (the last tile is turn's predecessor)
+        // the run's end: the group of its last tile (turn's predecessor) writes the
+        // result; the others go on
         xl[128 * g] = make_float2(l, ref);
-        {
-            const int pg = turn.g == 0 ? kGroups - 1 : turn.g - 1;
-            if (!warp_wait(bars.o_done(pg), turn.g == 0 ? turn.ph ^ 1u : turn.ph, abort)) return;
-        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.meet(), 1u);
-        if (!warp_wait(bars.meet(), static_cast<uint32_t>(k & 1), abort)) return;
+        if (lane == 0) mbar_arrive(bars.meet(k), 1u);
+        const int pg = turn.g == 0 ? kGroups - 1 : turn.g - 1;
+        if (g != pg) {
+            if (lane == 0) mbar_arrive(bars.item_empty(kb), 1u);
+            continue;
+        }
+        if (!warp_wait(bars.o_done(pg), turn.g == 0 ? turn.ph ^ 1u : turn.ph, abort) ||
+            !warp_wait(bars.meet(k), static_cast<uint32_t>((k >> 1) & 1), abort))
+            return;
         tc_fence_after();
         const float m = *xr;
         float sum = 0.f;
@@ -580,9 +589,8 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
         const int64_t row = static_cast<int64_t>(it.q0 + (live ? rr / a.G : 0)) * a.Hq +
                             it.hk * a.G + (live ? rr % a.G : 0);
         const float inv = __fdiv_rn(1.f, sum);
-        // columns in runs of 16, in turn
 #pragma unroll 1
-        for (int d = 16 * g; d < a.Dv; d += 16 * kGroups) {
+        for (int d = 0; d < a.Dv; d += 16) {
             float o[16];
             tmem_ldn<16>(tO + d, o);
             if (odds && live) {  // what was cleared: from memory, into the rows that see it
@@ -623,7 +631,7 @@ __device__ void softmax_warps(const PagedTcParams& p, unsigned char* smem, Bars 
             }
             __syncwarp();
         }
-        if (!whole && live && g == 0) {
+        if (!whole && live) {
             p.part_ml[2 * (slot * kRows + r)] = m;
             p.part_ml[2 * (slot * kRows + r) + 1] = bad ? -1.f : sum;
         }
@@ -664,12 +672,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         }
         for (int w = 0; w < 4; ++w)
             for (int g = 0; g < kGroups; ++g) mbar_init(bars.decide(w, g), 1u);
-        mbar_init(bars.meet(), kSoft);
-        mbar_init(bars.o_free(), kSoft);
+        mbar_init(bars.meet(0), kSoft);
+        mbar_init(bars.meet(1), kSoft);
+        mbar_init(bars.o_free(), 4u);  // the group that read it
         mbar_init(bars.drained(), 2u);
         *abort = 0;
         *reinterpret_cast<volatile int*>(smem + kOdd) = 0;
         *reinterpret_cast<volatile int*>(smem + kOdd + 4) = 0;
+        *reinterpret_cast<volatile int*>(smem + kOdd + 8) = 0;
         fence_mbar_init();
         prefetch_map(&p.tk);
         prefetch_map(&p.tv);
