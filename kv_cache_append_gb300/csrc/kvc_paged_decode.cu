@@ -40,9 +40,9 @@
 // memory, to the rows that see them.
 //
 // Measured: 64 tokens over 1024 to 8190 slots, 32 heads on 8 of 128, e4m3 pool (602 MB):
-// 113.5 us, 5300 GB/s, bounded by DRAM and 10 to 15 us of start and tail (4.2 GB of
+// 108.5 us, 5550 GB/s, bounded by DRAM and about 10 us of start and tail (4.2 GB of
 // cache: 6580 GB/s); 64 sequences of 1 to 4 tokens, cap, window 4096, bf16 pool (935 MB):
-// 196 us, 4770 GB/s, bounded by a tile's softmax chain with three stages an SM.
+// 172 us, 5430 GB/s, bounded by a tile's softmax chain with three stages an SM.
 #include <algorithm>
 #include <type_traits>
 

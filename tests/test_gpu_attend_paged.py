@@ -458,3 +458,24 @@ def test_two_calls_at_once(pool):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(ox, wx) and torch.equal(oz, wz)
+
+
+@pytest.mark.parametrize("dtype,pool,D", [("bf16", "e4m3", 128), ("f16", "f16", 64),
+                                          ("f16", "e5m2", 192)])
+def test_many_short_units_a_block(dtype, pool, D):
+    """Units of one to three tiles, several in each thread block: its groups work
+    on up to three units at once; the same bits every time, the timeout bit clear."""
+    r = random.Random(41)
+    lens = [(s, s + r.randint(0, 260)) for s in (r.randint(9, 70) for _ in range(90))]
+    x = make(41, dtype, pool, lens, 16, 4, D, 64, 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = kvc.attention_over_paged_cache(**x, max_seqlen_q=70, status=status)
+    assert int(status) == 0
+    check(x, got, 70)
+    for _ in range(10):
+        assert torch.equal(kvc.attention_over_paged_cache(**x, max_seqlen_q=70, status=status), got)
+    assert int(status) == 0
+    got = kvc.attention_over_paged_cache(**x, max_seqlen_q=70, window=100, softcap=8.0,
+                                         status=status)
+    assert int(status) == 0
+    check(x, got, 70, window=100, softcap=8.0)
