@@ -440,28 +440,42 @@ __device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const Paged
         if (mul && part == 0) mul[r] = a.scale;
         return;
     }
-    auto word2 = [&](int d) {  // four elements
-        return live && d < a.D ? *reinterpret_cast<const uint2*>(q + d) : make_uint2(0u, 0u);
+    // eight elements, in one load where every row starts on a 16-byte boundary
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.q) | static_cast<uintptr_t>(2 * a.q_tok) |
+                        static_cast<uintptr_t>(2 * a.q_head)) & 15u) == 0u;
+    auto words = [&](int d) {
+        if (!live || d >= a.D) return make_uint4(0u, 0u, 0u, 0u);
+        if (wide) return *reinterpret_cast<const uint4*>(q + d);
+        const uint2 x = *reinterpret_cast<const uint2*>(q + d), y = *reinterpret_cast<const uint2*>(q + d + 4);
+        return make_uint4(x.x, x.y, y.x, y.y);
     };
     constexpr uint32_t kInf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
-    uint32_t big = 0;  // the largest finite magnitude, as its 16 bits
-#pragma unroll 2
-    for (int c = part; c < nch; c += kPerRow) {
-        uint2 v[4];
+    // the largest magnitude, as its 16 bits, of either half of the words
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int c = part; c < 2 * nch; c += kPerRow) {
+        const uint4 v = words(c * 8);
+        const uint32_t m = 0x7fff7fffu;
+        top = __vmaxu2(__vmaxu2(top, v.x & m), __vmaxu2(v.y & m, __vmaxu2(v.z & m, v.w & m)));
+    }
+    uint32_t big = max(top & 0xffffu, top >> 16);
+    if (kPerRow == 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, 16));
+    const bool odd = big >= kInf;  // infinities or NaN: the largest finite one
+    if (__any_sync(0xffffffffu, odd)) {
+        uint32_t fin = 0;
+#pragma unroll 1
+        for (int c = part; c < 2 * nch; c += kPerRow) {
+            const uint4 v = words(c * 8);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = word2(c * 16 + e * 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t w[2] = {v[e].x, v[e].y};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t lo = w[h] & 0x7fffu, hi = (w[h] >> 16) & 0x7fffu;
-                if (lo < kInf) big = max(big, lo);
-                if (hi < kInf) big = max(big, hi);
+            for (int h = 0; h < 8; ++h) {
+                const uint32_t x = (w[h >> 1] >> (16 * (h & 1))) & 0x7fffu;
+                if (x < kInf) fin = max(fin, x);
             }
         }
+        if (kPerRow == 2) fin = max(fin, __shfl_xor_sync(0xffffffffu, fin, 16));
+        big = fin;
     }
-    if (kPerRow == 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, 16));
     const unsigned short raw = static_cast<unsigned short>(big);
     const float bigf = Storage<T>::to_float(*reinterpret_cast<const T*>(&raw));
     int e2 = 7 - (static_cast<int>(__float_as_uint(bigf) >> 23) - 127);
@@ -472,26 +486,34 @@ __device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const Paged
         constexpr int NP = QueryParts<T, 1>::v;
         uint32_t w[NP][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint2 v = word2(c * 16 + e * 4);
-            const T* x = reinterpret_cast<const T*>(&v);
-            float y[4];
+        for (int e = 0; e < 4; e += 2) {
+            const uint4 v = words(c * 16 + e * 4);
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+            // in fp16, which holds the scaled elements down to 2^-32 of the largest
+            __half2 y[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                y[k] = Storage<T>::to_float(x[k]) * f;
-                if (!(fabsf(y[k]) < INFINITY)) y[k] = __uint_as_float(0x7fffffffu);  // no infinity: NaN
+                const T* x = reinterpret_cast<const T*>(&vw[k]);
+                float y0 = Storage<T>::to_float(x[0]) * f, y1 = Storage<T>::to_float(x[1]) * f;
+                if (odd) {  // no infinity: NaN
+                    if (!(fabsf(y0) < INFINITY)) y0 = __uint_as_float(0x7fffffffu);
+                    if (!(fabsf(y1) < INFINITY)) y1 = __uint_as_float(0x7fffffffu);
+                }
+                y[k] = __floats2half2_rn(y0, y1);
             }
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
-                const uint32_t h0 = to_eight2<false>(y[0], y[1]), h1 = to_eight2<false>(y[2], y[3]);
-                w[n][e] = h0 | (h1 << 16);
-                if (n + 1 < NP) {  // what is left, exactly
-                    const float2 f0 = from_eight2<false>(h0), f1 = from_eight2<false>(h1);
-                    y[0] -= f0.x;
-                    y[1] -= f0.y;
-                    y[2] -= f1.x;
-                    y[3] -= f1.y;
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h[k] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(y[k]), __NV_SATFINITE,
+                                                      __NV_E4M3);
+                    if (n + 1 < NP)  // what is left, exactly
+                        y[k] = __hsub2(y[k], __half2(__nv_cvt_fp8x2_to_halfraw2(
+                                                 static_cast<__nv_fp8x2_storage_t>(h[k]), __NV_E4M3)));
                 }
+                w[n][e] = h[0] | (h[1] << 16);
+                w[n][e + 1] = h[2] | (h[3] << 16);
             }
         }
         unsigned char* o = dst + (c >> 3) * blk + (((c & 7) ^ (r & 7)) << 4);
