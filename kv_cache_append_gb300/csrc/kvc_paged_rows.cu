@@ -32,7 +32,7 @@
 // run's query rows.
 //
 // Measured, 32 heads on 8 of 128, four prompts of 513 to 2001 tokens over up to 8190
-// slots (617 GFLOP): e4m3 pool 748 us, 824 TFLOP/s, bf16 pool 640 us; bounded by the
+// slots (617 GFLOP): e4m3 pool 752 us, 820 TFLOP/s, bf16 pool 640 us; bounded by the
 // softmax warps' instruction fetch and issue (a tile takes about 2600 cycles where its
 // products take 1280 and 1024) and by a unit's start and end, the time of about 7 tiles.
 #include <algorithm>

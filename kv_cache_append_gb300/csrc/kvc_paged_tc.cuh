@@ -414,8 +414,10 @@ struct QueryParts {
 // two for a row (rows past the unit's are zero). 8-bit products: the parts one after
 // the other, of the row times the power of two that takes its largest element into
 // [2^7, 2^8) (what is under 2^-17 of that is lost); mul[r] is the score scale over
-// that power. (A warp for a row at a time
-// needed a reduction and a division for each: 45 us for 128 rows of 192.)
+// that power. (128 rows of 192: a warp for a row at a time needed a reduction and a
+// division for each, 45 us. 128 rows of 128 take 18,000 cycles, most of them latency of the
+// four warps' loads and conversions; eight threads a row, with four rows' or the next row's
+// loads ahead, spilled and were slower: 34.0 against 32.6 us for a unit of 16 tiles.)
 template <typename T, int EB, int ROWS, int THREADS>
 __device__ __forceinline__ void prepare_rows(const PagedTcParams& p, const PagedItem& it,
                                              unsigned char* sq, int nkb, int blk, int tid, float* mul) {
